@@ -296,6 +296,109 @@ dyra_status dyra_dense_ref(const void *X, const void *Wt, int64_t N, int64_t c1,
                            dyra_dtype dtype, void *Y, void *stream);
 
 /*
+ * ---- The feed-forward layer around the products --------------------------
+ *
+ * Exact products with their epilogues, and a mixture-of-experts layer for few
+ * tokens.  These calls need no plan.  All matrices are row-major with the rows
+ * `ld...` elements apart; weights are in the nn.Linear layout (output features
+ * by input features).  Products accumulate in float32, epilogues run in
+ * float32, and an output is rounded once.  Every call is asynchronous: it
+ * enqueues kernels on `stream` (NULL = the default stream), which must belong
+ * to the current device and to the device of the pointers, allocates nothing
+ * and does not synchronise, so it may be captured into a graph.  An output must
+ * not overlap an input, except that Y may be the residual itself (same pointer
+ * and row stride).
+ */
+typedef enum {
+    DYRA_ACT_NONE = 0,
+    DYRA_ACT_RELU = 1,
+    DYRA_ACT_GELU = 2,       /* v/2 (1 + erf(v / sqrt 2)) */
+    DYRA_ACT_GELU_TANH = 3,  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+    DYRA_ACT_SILU = 4        /* v / (1 + exp(-v)) */
+} dyra_act;
+
+/*
+ * Linear layer: Y = act(X W + bias) + residual.
+ *
+ * X         device, dtype, [N][c1].  c1 must be a whole number of 16-byte
+ *           chunks (a multiple of 8 for bf16, 4 for float32; DYRA_ERR_SHAPE
+ *           otherwise).
+ * Wt        device, dtype, [c2][c1] (W transposed).  c2 is any number >= 1.
+ * bias      device, dtype, [c2], or NULL.
+ * residual  device, out_dtype, [N][c2], or NULL; ldr = 0 adds the same row to
+ *           every token.
+ * Y         device, out_dtype, [N][c2]; elements between the rows are left as
+ *           they are.
+ * dtype     DYRA_BF16 with out_dtype DYRA_BF16 or DYRA_F32, or DYRA_F32 with
+ *           out_dtype DYRA_F32 (DYRA_ERR_DTYPE otherwise).
+ * N >= 0 (0 is a no-op); N, c1, c2 <= 2^30.  X, Wt and their row strides are
+ * 16-byte aligned, the others aligned to their elements (DYRA_ERR_ALIGN); a row
+ * stride below the row's length is DYRA_ERR_ARG.
+ */
+dyra_status dyra_linear(const void *X, int64_t ldx, const void *Wt, int64_t ldw, int64_t N, int64_t c1,
+                        int64_t c2, dyra_dtype dtype, const void *bias, dyra_act act, const void *residual,
+                        int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *stream);
+
+/*
+ * Gated pair of products: H = act(X Wg + bias_g) * (X Wu + bias_u), elementwise
+ * (SwiGLU for DYRA_ACT_SILU).  Wg and Wu device [c2][c1], rows ldw apart;
+ * H device, dtype, [N][c2].  Everything else as for dyra_linear.
+ */
+dyra_status dyra_gated(const void *X, int64_t ldx, const void *Wg, const void *Wu, int64_t ldw, int64_t N,
+                       int64_t c1, int64_t c2, dyra_dtype dtype, const void *bias_g, const void *bias_u,
+                       dyra_act act, void *H, int64_t ldh, void *stream);
+
+typedef enum {
+    DYRA_SCORE_SOFTMAX = 0,  /* exp(l_e) / sum over all experts */
+    DYRA_SCORE_SIGMOID = 1   /* 1 / (1 + exp(-l_e)) */
+} dyra_score;
+
+/*
+ * Router of a mixture-of-experts layer: for every row of logits (device, dtype,
+ * [T][experts]) the topk largest, in descending order, equal ones by ascending
+ * index, and their scores.
+ *
+ * ids      device int32 [T][topk].
+ * weights  device float32 [T][topk]: the scores, divided by their sum over the
+ *          row's topk if renormalise is not 0, then times scale (finite).
+ * A logit of -inf (a masked expert) or NaN is never chosen and adds nothing to
+ * the softmax; places that are left over hold the id -1 and the weight 0, so a
+ * row with every expert masked is all -1.  Experts at +inf share the softmax.
+ * 1 <= topk <= min(experts, 64), experts <= 1024 (DYRA_ERR_SHAPE otherwise).
+ */
+dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t experts, int32_t topk,
+                       dyra_dtype dtype, dyra_score score, int32_t renormalise, float scale, int32_t *ids,
+                       float *weights, void *stream);
+
+/*
+ * Mixture-of-experts layer for few tokens (decoding batches):
+ *
+ *     Y[t] = residual[t] + sum_j weights[t][j] (act(X[t] Wg_e) * (X[t] Wu_e)) Wd_e,   e = ids[t][j]
+ *
+ * X         device, dtype, [T][c].  c and f whole numbers of 16-byte chunks.
+ * Wg, Wu    device, dtype, contiguous [experts][f][c];  Wd [experts][c][f].
+ * ids       device int32 [T][topk]; a place whose id is not in [0, experts)
+ *           adds nothing whatever its weight, an expert named twice counts twice.
+ * weights   device float32 [T][topk].
+ * residual  device, dtype, [T][c], or NULL; ldr = 0 adds the same row to every
+ *           token.
+ * Y         device, dtype, [T][c].
+ * workspace device, >= dyra_moe_workspace_bytes(T, topk, f, dtype) bytes,
+ *           contents on entry ignored; calls that overlap in time need separate
+ *           ones.  It holds the experts' inner activations in dtype.
+ * T * topk <= 1024, topk <= 64, experts <= 1024 (DYRA_ERR_SHAPE otherwise: more
+ * tokens go in several calls).  The sums of a token run in the order of its
+ * places, so equal calls give equal bits.
+ */
+dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f, const void *Wg,
+                     const void *Wu, const void *Wd, int32_t experts, const int32_t *ids, const float *weights,
+                     int32_t topk, dyra_dtype dtype, dyra_act act, const void *residual, int64_t ldr, void *Y,
+                     int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of dyra_moe; 0 for arguments it refuses (and for T = 0). */
+size_t dyra_moe_workspace_bytes(int64_t T, int32_t topk, int64_t f, dyra_dtype dtype);
+
+/*
  * Stage timing for measurement tools: as dyra_forward, but records
  * events[0..n_events) (hipEvent_t, created by the caller) on `stream` before
  * the first kernel and after each kernel of the path.  *n_recorded receives the

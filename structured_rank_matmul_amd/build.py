@@ -12,7 +12,8 @@ ROOT = os.path.dirname(PKG)
 OUT = os.path.join(PKG, "libdyra.so")
 BUILD = os.path.join(ROOT, "_build")
 
-HIP_SOURCES = ["dyra_api.hip", "gemm.hip", "solve.hip", "dyra_decode.hip", "als.hip", "ns.hip", "blast.hip"]
+HIP_SOURCES = ["dyra_api.hip", "gemm.hip", "solve.hip", "dyra_decode.hip", "als.hip", "ns.hip", "blast.hip",
+               "ffn_api.hip", "linear.hip", "skinny.hip", "moe.hip"]
 CXX_SOURCES = ["host_factorize.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

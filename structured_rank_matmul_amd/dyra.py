@@ -28,6 +28,7 @@ EXPORTED = (
     "dyra_workspace_bytes", "dyra_forward", "dyra_forward_ex", "dyra_forward_status", "dyra_dense_ref",
     "dyra_forward_timed", "dyra_stage_name", "dyra_prepare_blast", "dyra_factorize_blast_host",
     "dyra_forward_noalloc", "dyra_noalloc_scratch_bytes",
+    "dyra_linear", "dyra_gated", "dyra_route", "dyra_moe", "dyra_moe_workspace_bytes",
 )
 
 
@@ -87,6 +88,18 @@ def load() -> ctypes.CDLL:
     L.dyra_forward_noalloc.restype = ctypes.c_int
     L.dyra_noalloc_scratch_bytes.argtypes = []
     L.dyra_noalloc_scratch_bytes.restype = ctypes.c_size_t
+    en = ctypes.c_int
+    L.dyra_linear.argtypes = [vp, i64, vp, i64, i64, i64, i64, en, vp, en, vp, i64, en, vp, i64, vp]
+    L.dyra_linear.restype = ctypes.c_int
+    L.dyra_gated.argtypes = [vp, i64, vp, vp, i64, i64, i64, i64, en, vp, vp, en, vp, i64, vp]
+    L.dyra_gated.restype = ctypes.c_int
+    L.dyra_route.argtypes = [vp, i64, i64, i32, i32, en, en, i32, f32, vp, vp, vp]
+    L.dyra_route.restype = ctypes.c_int
+    L.dyra_moe.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, i32, vp, vp, i32, en, en, vp, i64, vp, i64, vp,
+                           ctypes.c_size_t, vp]
+    L.dyra_moe.restype = ctypes.c_int
+    L.dyra_moe_workspace_bytes.argtypes = [i64, i32, i64, en]
+    L.dyra_moe_workspace_bytes.restype = ctypes.c_size_t
     L.dyra_stage_name.argtypes = [vp, i64, i32]
     L.dyra_stage_name.restype = ctypes.c_char_p
     _lib = L
@@ -381,4 +394,165 @@ def dyra_dense_ref(X, Wt, Y=None, stream=None):
     st = load().dyra_dense_ref(_dev_ptr(X), _dev_ptr(Wt), N, c1, c2, _dtype_code(X.dtype), _dev_ptr(Y),
                                _stream_ptr(stream))
     _check(st, "dyra_dense_ref")
+    return Y
+
+
+# ------------------------------------------------------------------ feed-forward layer
+
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _named(table, name, what):
+    if name not in table:
+        raise ValueError(f"unknown {what} {name!r}; known: {sorted(table)}")
+    return table[name]
+
+
+def _matrix(t, name, X, rows, cols, dtype, broadcast=False):
+    """Checks a [rows, cols] matrix next to X and returns its row stride (0 for one row read by every token)."""
+    if t.dtype != dtype or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}] in {dtype}, got {tuple(t.shape)} in {t.dtype}")
+    if t.device != X.device:
+        raise ValueError(f"{name} is on {t.device}, X on {X.device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    if rows <= 1:
+        return cols
+    ld = t.stride(0)
+    if ld == 0 and not broadcast:
+        raise ValueError(f"{name} must not repeat one row")
+    return ld
+
+
+def _vector(t, name, X, n):
+    if t.dtype != X.dtype or tuple(t.shape) != (n,) or t.device != X.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{n}] in {X.dtype} on {X.device}")
+    return t.data_ptr()
+
+
+def _input(X, name="X"):
+    if not X.is_cuda:
+        raise ValueError("tensor must be on the GPU")
+    if X.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return _matrix(X, name, X, X.shape[0], X.shape[1], X.dtype)
+
+
+def _call(X, stream, what, call):
+    """call(stream pointer) with X's device current, so that the stream, the launch and the allocations agree."""
+    import torch
+    if stream is not None and stream.device != X.device:
+        raise ValueError(f"the stream is on {stream.device}, X on {X.device}")
+    if X.device.index == torch.cuda.current_device():
+        st = call((stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(X.device):
+            st = call((stream or torch.cuda.current_stream()).cuda_stream)
+    _check(st, what)
+
+
+def dyra_linear(X, Wt, bias=None, act: str = "none", residual=None, out_dtype=None, Y=None, stream=None):
+    """Y = act(X W + bias) + residual with Wt = W^T [c2, c1]; X [N, c1], residual and Y [N, c2] in out_dtype
+    (X's by default; float32 from bfloat16 operands too).  Rows may be strided; a residual expanded from
+    one row is added to every token, and Y may be the residual itself."""
+    import torch
+    ldx = _input(X)
+    N, c1 = X.shape
+    c2 = Wt.shape[0]
+    ldw = _matrix(Wt, "Wt", X, c2, c1, X.dtype)
+    out = X.dtype if out_dtype is None else out_dtype
+    if Y is None:
+        Y = torch.empty((N, c2), dtype=out, device=X.device)
+        _on_stream(Y, stream)
+        ldy = c2
+    else:
+        ldy = _matrix(Y, "Y", X, N, c2, out)
+    ldr = _matrix(residual, "residual", X, N, c2, out, broadcast=True) if residual is not None else 0
+    b = _vector(bias, "bias", X, c2) if bias is not None else None
+    a, dt, ot = _named(_ACTS, act, "activation"), _dtype_code(X.dtype), _dtype_code(out)
+    _call(X, stream, "dyra_linear", lambda s: load().dyra_linear(
+        X.data_ptr(), ldx, Wt.data_ptr(), ldw, N, c1, c2, dt, b, a,
+        residual.data_ptr() if residual is not None else None, ldr, ot, Y.data_ptr(), ldy, s))
+    return Y
+
+
+def dyra_gated(X, Wg, Wu, bias_g=None, bias_u=None, act: str = "silu", H=None, stream=None):
+    """H = act(X Wg + bias_g) * (X Wu + bias_u), the gate and up products of a gated MLP; Wg, Wu [c2, c1]
+    with one row stride."""
+    import torch
+    ldx = _input(X)
+    N, c1 = X.shape
+    c2 = Wg.shape[0]
+    ldw = _matrix(Wg, "Wg", X, c2, c1, X.dtype)
+    if _matrix(Wu, "Wu", X, c2, c1, X.dtype) != ldw:
+        raise ValueError("Wg and Wu must have one row stride")
+    if H is None:
+        H = torch.empty((N, c2), dtype=X.dtype, device=X.device)
+        _on_stream(H, stream)
+        ldh = c2
+    else:
+        ldh = _matrix(H, "H", X, N, c2, X.dtype)
+    bg = _vector(bias_g, "bias_g", X, c2) if bias_g is not None else None
+    bu = _vector(bias_u, "bias_u", X, c2) if bias_u is not None else None
+    a, dt = _named(_ACTS, act, "activation"), _dtype_code(X.dtype)
+    _call(X, stream, "dyra_gated", lambda s: load().dyra_gated(
+        X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, c1, c2, dt, bg, bu, a, H.data_ptr(), ldh, s))
+    return H
+
+
+def dyra_route(logits, topk: int, score: str = "softmax", renormalise: bool = True, scale: float = 1.0, stream=None):
+    """(ids int32, weights float32), both [T, topk]: the topk largest logits of every row and their scores.
+    Masked (-inf) experts are never chosen; places left over hold -1 and 0."""
+    import torch
+    ld = _input(logits, "logits")
+    T, experts = logits.shape
+    sc, dt = _named(_SCORES, score, "score"), _dtype_code(logits.dtype)
+    if not 1 <= int(topk) <= experts:
+        raise ValueError(f"topk must be in [1, {experts}]")
+    ids = torch.empty((T, int(topk)), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, int(topk)), dtype=torch.float32, device=logits.device)
+    _on_stream(ids, stream)
+    _on_stream(weights, stream)
+    _call(logits, stream, "dyra_route", lambda s: load().dyra_route(
+        logits.data_ptr(), ld, T, experts, int(topk), dt, sc, int(bool(renormalise)), float(scale), ids.data_ptr(),
+        weights.data_ptr(), s))
+    return ids, weights
+
+
+def dyra_moe_workspace_bytes(T: int, topk: int, f: int, dtype) -> int:
+    return int(load().dyra_moe_workspace_bytes(int(T), int(topk), int(f), _dtype_code(dtype)))
+
+
+def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=None, workspace=None, stream=None):
+    """Y = residual + sum over a token's places of weight * (act(X Wg_e) * (X Wu_e)) Wd_e, for few tokens:
+    X [T, c], Wg and Wu [experts, f, c], Wd [experts, c, f], ids (int32) and weights (float32) [T, topk]."""
+    import torch
+    ldx = _input(X)
+    T, c = X.shape
+    if Wg.dim() != 3 or ids.dim() != 2:
+        raise ValueError("Wg must be [experts, f, c] and ids [T, topk]")
+    experts, f, topk = Wg.shape[0], Wg.shape[1], ids.shape[1]
+    for t, name, shape, dtype in ((Wg, "Wg", (experts, f, c), X.dtype), (Wu, "Wu", (experts, f, c), X.dtype),
+                                  (Wd, "Wd", (experts, c, f), X.dtype), (ids, "ids", (T, topk), torch.int32),
+                                  (weights, "weights", (T, topk), torch.float32)):
+        if tuple(t.shape) != shape or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {list(shape)} in {dtype} on {X.device}")
+    a, dt = _named(_ACTS, act, "activation"), _dtype_code(X.dtype)
+    if Y is None:
+        Y = torch.empty((T, c), dtype=X.dtype, device=X.device)
+        _on_stream(Y, stream)
+        ldy = c
+    else:
+        ldy = _matrix(Y, "Y", X, T, c, X.dtype)
+    ldr = _matrix(residual, "residual", X, T, c, X.dtype, broadcast=True) if residual is not None else 0
+    if workspace is None:
+        workspace = torch.empty(max(T * topk * f * X.element_size(), 16), dtype=torch.uint8, device=X.device)
+        _on_stream(workspace, stream)
+    elif workspace.device != X.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {X.device}")
+    _call(X, stream, "dyra_moe", lambda s: load().dyra_moe(
+        X.data_ptr(), ldx, T, c, f, Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), experts, ids.data_ptr(),
+        weights.data_ptr(), topk, dt, a, residual.data_ptr() if residual is not None else None, ldr, Y.data_ptr(), ldy,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
     return Y

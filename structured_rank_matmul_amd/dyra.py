@@ -398,106 +398,126 @@ def dyra_dense_ref(X, Wt, Y=None, stream=None):
 
 
 # ------------------------------------------------------------------ feed-forward layer
+#
+# A call for one token runs a kernel of a few microseconds, so the checks below
+# are written for few Python operations: one read of each tensor property, the
+# raw stream pointer instead of a Stream object.
 
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_codes: dict = {}   # torch dtype -> dyra_dtype
 
 
-def _named(table, name, what):
-    if name not in table:
+def _code_of(dtype) -> int:
+    code = _codes.get(dtype)
+    if code is None:
+        code = _codes[dtype] = _dtype_code(dtype)
+    return code
+
+
+def _named(table, name, what) -> int:
+    code = table.get(name)
+    if code is None:
         raise ValueError(f"unknown {what} {name!r}; known: {sorted(table)}")
-    return table[name]
+    return code
 
 
-def _matrix(t, name, X, rows, cols, dtype, broadcast=False):
-    """Checks a [rows, cols] matrix next to X and returns its row stride (0 for one row read by every token)."""
-    if t.dtype != dtype or tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}] in {dtype}, got {tuple(t.shape)} in {t.dtype}")
-    if t.device != X.device:
-        raise ValueError(f"{name} is on {t.device}, X on {X.device}")
-    if cols > 1 and t.stride(1) != 1:
+def _input(X, name="X"):
+    """(rows, columns, row stride, device index) of the matrix a call works on."""
+    if X.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    dev = X.get_device()
+    if dev < 0:
+        raise ValueError("tensor must be on the GPU")
+    rows, cols = X.shape
+    return rows, cols, _matrix(X, name, dev, rows, cols, X.dtype), dev
+
+
+def _matrix(t, name, dev, rows, cols, dtype, broadcast=False) -> int:
+    """Checks a [rows, cols] matrix on device `dev`; its row stride (0 for one row read by every token)."""
+    if t.dtype != dtype or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}] in {dtype}, got {list(t.shape)} in {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, is on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
     if rows <= 1:
         return cols
-    ld = t.stride(0)
     if ld == 0 and not broadcast:
         raise ValueError(f"{name} must not repeat one row")
     return ld
 
 
-def _vector(t, name, X, n):
-    if t.dtype != X.dtype or tuple(t.shape) != (n,) or t.device != X.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [{n}] in {X.dtype} on {X.device}")
+def _whole(t, name, dev, shape, dtype) -> int:
+    """Checks a contiguous tensor of that shape on device `dev`; its address."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)} in {dtype} on GPU {dev}")
     return t.data_ptr()
 
 
-def _input(X, name="X"):
-    if not X.is_cuda:
-        raise ValueError("tensor must be on the GPU")
-    if X.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    return _matrix(X, name, X, X.shape[0], X.shape[1], X.dtype)
+def _new(shape, dtype, X, stream):
+    t = X.new_empty(shape) if dtype == X.dtype else X.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        _on_stream(t, stream)
+    return t
 
 
-def _call(X, stream, what, call):
-    """call(stream pointer) with X's device current, so that the stream, the launch and the allocations agree."""
+def _run(fn, what, dev, stream, *args) -> None:
+    """fn(*args, stream) with device `dev` current, so that the stream and the launch agree."""
     import torch
-    if stream is not None and stream.device != X.device:
-        raise ValueError(f"the stream is on {stream.device}, X on {X.device}")
-    if X.device.index == torch.cuda.current_device():
-        st = call((stream or torch.cuda.current_stream()).cuda_stream)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {dev}")
     else:
-        with torch.cuda.device(X.device):
-            st = call((stream or torch.cuda.current_stream()).cuda_stream)
-    _check(st, what)
+        st = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status != 0:
+        raise DyraError(status, what)
 
 
 def dyra_linear(X, Wt, bias=None, act: str = "none", residual=None, out_dtype=None, Y=None, stream=None):
     """Y = act(X W + bias) + residual with Wt = W^T [c2, c1]; X [N, c1], residual and Y [N, c2] in out_dtype
     (X's by default; float32 from bfloat16 operands too).  Rows may be strided; a residual expanded from
     one row is added to every token, and Y may be the residual itself."""
-    import torch
-    ldx = _input(X)
-    N, c1 = X.shape
-    c2 = Wt.shape[0]
-    ldw = _matrix(Wt, "Wt", X, c2, c1, X.dtype)
-    out = X.dtype if out_dtype is None else out_dtype
+    N, c1, ldx, dev = _input(X)
+    t, c2 = X.dtype, Wt.shape[0]
+    out = t if out_dtype is None else out_dtype
+    ldw = _matrix(Wt, "Wt", dev, c2, c1, t)
+    b = None if bias is None else _whole(bias, "bias", dev, (c2,), t)
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c2, out, True)
     if Y is None:
-        Y = torch.empty((N, c2), dtype=out, device=X.device)
-        _on_stream(Y, stream)
-        ldy = c2
+        Y, ldy = _new((N, c2), out, X, stream), c2
     else:
-        ldy = _matrix(Y, "Y", X, N, c2, out)
-    ldr = _matrix(residual, "residual", X, N, c2, out, broadcast=True) if residual is not None else 0
-    b = _vector(bias, "bias", X, c2) if bias is not None else None
-    a, dt, ot = _named(_ACTS, act, "activation"), _dtype_code(X.dtype), _dtype_code(out)
-    _call(X, stream, "dyra_linear", lambda s: load().dyra_linear(
-        X.data_ptr(), ldx, Wt.data_ptr(), ldw, N, c1, c2, dt, b, a,
-        residual.data_ptr() if residual is not None else None, ldr, ot, Y.data_ptr(), ldy, s))
+        ldy = _matrix(Y, "Y", dev, N, c2, out)
+    _run((_lib or load()).dyra_linear, "dyra_linear", dev, stream, X.data_ptr(), ldx, Wt.data_ptr(), ldw, N, c1, c2,
+         _code_of(t), b, _named(_ACTS, act, "activation"), r, ldr, _code_of(out), Y.data_ptr(), ldy)
     return Y
 
 
 def dyra_gated(X, Wg, Wu, bias_g=None, bias_u=None, act: str = "silu", H=None, stream=None):
     """H = act(X Wg + bias_g) * (X Wu + bias_u), the gate and up products of a gated MLP; Wg, Wu [c2, c1]
     with one row stride."""
-    import torch
-    ldx = _input(X)
-    N, c1 = X.shape
-    c2 = Wg.shape[0]
-    ldw = _matrix(Wg, "Wg", X, c2, c1, X.dtype)
-    if _matrix(Wu, "Wu", X, c2, c1, X.dtype) != ldw:
+    N, c1, ldx, dev = _input(X)
+    t, c2 = X.dtype, Wg.shape[0]
+    ldw = _matrix(Wg, "Wg", dev, c2, c1, t)
+    if _matrix(Wu, "Wu", dev, c2, c1, t) != ldw:
         raise ValueError("Wg and Wu must have one row stride")
+    bg = None if bias_g is None else _whole(bias_g, "bias_g", dev, (c2,), t)
+    bu = None if bias_u is None else _whole(bias_u, "bias_u", dev, (c2,), t)
     if H is None:
-        H = torch.empty((N, c2), dtype=X.dtype, device=X.device)
-        _on_stream(H, stream)
-        ldh = c2
+        H, ldh = _new((N, c2), t, X, stream), c2
     else:
-        ldh = _matrix(H, "H", X, N, c2, X.dtype)
-    bg = _vector(bias_g, "bias_g", X, c2) if bias_g is not None else None
-    bu = _vector(bias_u, "bias_u", X, c2) if bias_u is not None else None
-    a, dt = _named(_ACTS, act, "activation"), _dtype_code(X.dtype)
-    _call(X, stream, "dyra_gated", lambda s: load().dyra_gated(
-        X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, c1, c2, dt, bg, bu, a, H.data_ptr(), ldh, s))
+        ldh = _matrix(H, "H", dev, N, c2, t)
+    _run((_lib or load()).dyra_gated, "dyra_gated", dev, stream, X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N,
+         c1, c2, _code_of(t), bg, bu, _named(_ACTS, act, "activation"), H.data_ptr(), ldh)
     return H
 
 
@@ -505,18 +525,14 @@ def dyra_route(logits, topk: int, score: str = "softmax", renormalise: bool = Tr
     """(ids int32, weights float32), both [T, topk]: the topk largest logits of every row and their scores.
     Masked (-inf) experts are never chosen; places left over hold -1 and 0."""
     import torch
-    ld = _input(logits, "logits")
-    T, experts = logits.shape
-    sc, dt = _named(_SCORES, score, "score"), _dtype_code(logits.dtype)
-    if not 1 <= int(topk) <= experts:
+    T, experts, ld, dev = _input(logits, "logits")
+    if not 1 <= topk <= experts:
         raise ValueError(f"topk must be in [1, {experts}]")
-    ids = torch.empty((T, int(topk)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, int(topk)), dtype=torch.float32, device=logits.device)
-    _on_stream(ids, stream)
-    _on_stream(weights, stream)
-    _call(logits, stream, "dyra_route", lambda s: load().dyra_route(
-        logits.data_ptr(), ld, T, experts, int(topk), dt, sc, int(bool(renormalise)), float(scale), ids.data_ptr(),
-        weights.data_ptr(), s))
+    ids = _new((T, topk), torch.int32, logits, stream)
+    weights = _new((T, topk), torch.float32, logits, stream)
+    _run((_lib or load()).dyra_route, "dyra_route", dev, stream, logits.data_ptr(), ld, T, experts, topk,
+         _code_of(logits.dtype), _named(_SCORES, score, "score"), 1 if renormalise else 0, scale, ids.data_ptr(),
+         weights.data_ptr())
     return ids, weights
 
 
@@ -528,31 +544,29 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     """Y = residual + sum over a token's places of weight * (act(X Wg_e) * (X Wu_e)) Wd_e, for few tokens:
     X [T, c], Wg and Wu [experts, f, c], Wd [experts, c, f], ids (int32) and weights (float32) [T, topk]."""
     import torch
-    ldx = _input(X)
-    T, c = X.shape
+    T, c, ldx, dev = _input(X)
+    t = X.dtype
     if Wg.dim() != 3 or ids.dim() != 2:
         raise ValueError("Wg must be [experts, f, c] and ids [T, topk]")
-    experts, f, topk = Wg.shape[0], Wg.shape[1], ids.shape[1]
-    for t, name, shape, dtype in ((Wg, "Wg", (experts, f, c), X.dtype), (Wu, "Wu", (experts, f, c), X.dtype),
-                                  (Wd, "Wd", (experts, c, f), X.dtype), (ids, "ids", (T, topk), torch.int32),
-                                  (weights, "weights", (T, topk), torch.float32)):
-        if tuple(t.shape) != shape or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {list(shape)} in {dtype} on {X.device}")
-    a, dt = _named(_ACTS, act, "activation"), _dtype_code(X.dtype)
+    experts, f, _ = Wg.shape
+    topk = ids.shape[1]
+    g = _whole(Wg, "Wg", dev, (experts, f, c), t)
+    u = _whole(Wu, "Wu", dev, (experts, f, c), t)
+    d = _whole(Wd, "Wd", dev, (experts, c, f), t)
+    i = _whole(ids, "ids", dev, (T, topk), torch.int32)
+    w = _whole(weights, "weights", dev, (T, topk), torch.float32)
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, T, c, t, True)
     if Y is None:
-        Y = torch.empty((T, c), dtype=X.dtype, device=X.device)
-        _on_stream(Y, stream)
-        ldy = c
+        Y, ldy = _new((T, c), t, X, stream), c
     else:
-        ldy = _matrix(Y, "Y", X, T, c, X.dtype)
-    ldr = _matrix(residual, "residual", X, T, c, X.dtype, broadcast=True) if residual is not None else 0
+        ldy = _matrix(Y, "Y", dev, T, c, t)
     if workspace is None:
-        workspace = torch.empty(max(T * topk * f * X.element_size(), 16), dtype=torch.uint8, device=X.device)
-        _on_stream(workspace, stream)
-    elif workspace.device != X.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {X.device}")
-    _call(X, stream, "dyra_moe", lambda s: load().dyra_moe(
-        X.data_ptr(), ldx, T, c, f, Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), experts, ids.data_ptr(),
-        weights.data_ptr(), topk, dt, a, residual.data_ptr() if residual is not None else None, ldr, Y.data_ptr(), ldy,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+        workspace = _new((max(T * topk * f, 16),), t, X, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on GPU {dev}")
+    _run((_lib or load()).dyra_moe, "dyra_moe", dev, stream, X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk,
+         _code_of(t), _named(_ACTS, act, "activation"), r, ldr, Y.data_ptr(), ldy, workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
     return Y

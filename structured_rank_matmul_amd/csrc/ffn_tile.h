@@ -14,6 +14,8 @@
 #include "ffn_kernels.h"
 #include "mfma_tile.h"
 
+#include <type_traits>
+
 namespace dyra {
 
 __device__ __forceinline__ f32x4 mma32(f32x4 acc, bf16x8 a, bf16x8 b) {

@@ -18,7 +18,7 @@
 // (block q, row i holds feature 8 (i / 4) + 4 q + i % 4 of the pair's 32): the
 // epilogue stores 16 bytes per lane straight from registers, 64 bytes of a row
 // per instruction, with no pass through LDS.
-#include "ffn_tile.h"
+#include "linear_big.h"
 
 #include <algorithm>
 #include <cmath>
@@ -184,6 +184,10 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
+    if constexpr (sizeof(E) == 2) {
+        const int64_t t256 = ((a.M + 255) / 256) * ((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
+        if (t256 >= 128 && a.ldx <= (1 << 22) && a.ldw <= (1 << 22)) return launch_big<O, GATED>(a, st);
+    }
     const int64_t big = ((a.M + 127) / 128) * ((a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
     if (big >= 192) return launch_tile<E, O, 128, GATED ? 64 : 128, 2, 2, 2, GATED>(a, st);
     return launch_tile<E, O, 64, GATED ? 32 : 64, 4, 1, 3, GATED>(a, st);

@@ -124,6 +124,24 @@ def test_gated(N, c1, c2, dtype):
         close(h, *gated_ref(x, wg, wu, bg if bias else None, bu if bias else None, act, t), f"{act} {bias}")
 
 
+# enough 256 x 256 tiles to fill the chip; one to six slabs of K, whole and partial; rows and features past the last tile
+@pytest.mark.parametrize("N,c1,c2", [(4000, 8, 2050), (3841, 64, 2304), (4096, 72, 2048), (4100, 128, 2001), (3900, 192, 2100),
+                                     (2100, 264, 4000), (4097, 320, 1930), (33000, 40, 100)])
+def test_many_tiles(N, c1, c2):
+    import torch
+    t = torch.bfloat16
+    x, w, w2 = rand((N, c1), 81, t), rand((c2, c1), 82, t, c1 ** -0.5), rand((c2, c1), 83, t, c1 ** -0.5)
+    b, r = rand((c2,), 84, t), rand((N, c2), 85, t)
+    xd, wd, w2d, bd, rd = (v.cuda() for v in (x, w, w2, b, r))
+    close(dyra.dyra_linear(xd, wd, bias=bd, act="gelu", residual=rd), *linear_ref(x, w, b, "gelu", r, t))
+    close(dyra.dyra_linear(xd, wd, out_dtype=torch.float32), *linear_ref(x, w, None, "none", None, torch.float32))
+    close(dyra.dyra_gated(xd, wd, w2d, bias_u=bd), *gated_ref(x, w, w2, None, b, "silu", t))
+    if c1 > 8:   # a column slice: rows further apart than they are long
+        k = c1 // 2 // 8 * 8
+        y = dyra.dyra_linear(xd[:, 8:8 + k], wd[:, :k])
+        close(y, *linear_ref(x[:, 8:8 + k], w[:, :k], None, "none", None, t))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [3, 50, 200, 400])
 def test_strided_rows_and_untouched_gaps(N, dtype):

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = acc[i][2 * p + (q >> 2)][q & 3] + b0[q];
-            activate(v, a.act);
+            activate<sizeof(O) == 4>(v, a.act);
             if constexpr (GATED) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= acc[i][S::TF + 2 * p + (q >> 2)][q & 3] + b1[q];

@@ -8,29 +8,26 @@
 // bytes per row) through two LDS buffers.  A slab is four phases, one per
 // quadrant (token half x weight half) of the wavefront's block, 16 MFMAs each:
 //
-//     phase   reads into registers       product      copies of slab s + 2
-//     0       tokens A (8 x 16 B)         A x weights A    weights A
-//     1       weights B (4)               A x weights B    tokens A
-//     2       tokens B (8)                B x weights B    weights B
-//     3       weights A of slab s + 1 (4) B x weights A    tokens B
+//     phase   reads into registers       product         copies
+//     0       tokens A (8 x 16 B)         A x weights A   tokens B of slab s + 1
+//     1       weights B (4)               A x weights B   weights A of slab s + 2
+//     2       tokens B (8)                B x weights B   tokens A of slab s + 2
+//     3       weights A of slab s + 1 (4) B x weights A   weights B of slab s + 2
 //
-// A phase is [reads, copies, waits] barrier [MFMAs] barrier, and the second
+// A phase is [reads, copies, wait] barrier [MFMAs] barrier, and the second
 // group (wm = 1, sharing each SIMD with the first) runs one barrier behind, so
 // that one group's MFMAs cover the other's reads.  A region of a buffer is
-// copied over one phase after its last read: every read is waited for before
-// the barrier that ends its half of the phase.  A copy has six phases to land:
-// each half phase waits until at most 12 newer copies are outstanding, and the
-// barrier after it publishes them.
+// copied over two phases after its last read was issued: the read has then been
+// waited for by MFMAs that every wavefront finished a barrier before.  A copy
+// has five phases to land: each phase waits until at most 10 newer copies are
+// outstanding, and the barrier after it publishes them.
 #pragma once
 
 #include "ffn_tile.h"
 
 namespace dyra {
 
-template <int N> __device__ __forceinline__ void wait_lds_and_vm() {
-    // lgkmcnt(0) and vmcnt(N): gfx9 encoding, expcnt left at its maximum
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
+template <int N> using ic = std::integral_constant<int, N>;
 
 template <typename O, bool GATED>
 __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> a, int tiles_m, int tiles_n,
@@ -159,35 +156,35 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         __builtin_amdgcn_sched_barrier(0);
         barrier_only();
     };
-    // One slab; A: the slot that holds weights A.  The last two slabs have
-    // nothing to copy ahead and wait for every copy instead.
+    // One slab; A: the slot that holds weights A.  In the last two slabs fewer
+    // copies are outstanding: LAST2 and LAST1 of them are newer than the one the
+    // next phase reads.
     auto slab = [&](int s, auto slot_a) __attribute__((always_inline)) {
         constexpr int A = decltype(slot_a)::value, B = 1 - A;
-        const bool ahead = s + 2 < slabs, mask = s + 1 == slabs && rem < 128;
-        auto half_phase = [&](auto copy) __attribute__((always_inline)) {
-            if (ahead) {
-                copy();
-                wait_lds_and_vm<12>();
-            } else {
-                wait_lds_and_vm<0>();
-            }
+        const int ahead = slabs - 1 - s;  // slabs after this one
+        const bool mask = ahead == 0 && rem < 128;
+        auto landed = [&](auto last2, auto last1) __attribute__((always_inline)) {
+            if (ahead >= 2) wait_vmcnt<10>();
+            else if (ahead == 1) wait_vmcnt<decltype(last2)::value>();
+            else wait_vmcnt<decltype(last1)::value>();
         };
         read_x(s, 0);
-        half_phase([&]() __attribute__((always_inline)) { copy_w(s + 2, 0); });
+        if (ahead >= 1) copy_x(s + 1, 1);
+        landed(ic<10>{}, ic<2>{});
         products(0, 0, A, mask);
         read_w(s, 1, B);
-        half_phase([&]() __attribute__((always_inline)) { copy_x(s + 2, 0); });
+        if (ahead >= 2) copy_w(s + 2, 0);
+        landed(ic<8>{}, ic<0>{});
         products(0, 1, B, mask);
         read_x(s, 1);
-        half_phase([&]() __attribute__((always_inline)) { copy_w(s + 2, 1); });
+        if (ahead >= 2) copy_x(s + 2, 0);
+        landed(ic<6>{}, ic<0>{});
         products(1, 1, B, mask);
         read_w(s + 1, 0, B);  // past the last slab: a buffer's old bytes, not used
-        half_phase([&]() __attribute__((always_inline)) { copy_x(s + 2, 1); });
+        if (ahead >= 2) copy_w(s + 2, 1);
+        landed(ic<4>{}, ic<0>{});
         products(1, 0, A, mask);
     };
-    constexpr std::integral_constant<int, 0> c0{};
-    constexpr std::integral_constant<int, 1> c1{};
-
     copy_w(0, 0);
     copy_x(0, 0);
     copy_w(0, 1);
@@ -196,19 +193,16 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         copy_w(1, 0);
         copy_x(1, 0);
         copy_w(1, 1);
-        copy_x(1, 1);
-        wait_lds_and_vm<12>();
+        wait_vmcnt<10>();
     } else {
-        wait_lds_and_vm<4>();
+        wait_vmcnt<4>();
     }
     barrier_only();
     read_w(0, 0, 0);
-    wait_lds_and_vm<12>();
-    barrier_only();
     if (wm == 1) barrier_only();
     for (int s = 0; s < slabs; s += 2) {
-        slab(s, c0);
-        if (s + 1 < slabs) slab(s + 1, c1);
+        slab(s, ic<0>{});
+        if (s + 1 < slabs) slab(s + 1, ic<1>{});
     }
     if (wm == 0) barrier_only();
 
@@ -230,7 +224,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
                 float v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = acc[hx][hw][i][q >> 2][q & 3] + b0[q];
-                activate(v, a.act);
+                activate<sizeof(O) == 4>(v, a.act);
                 if constexpr (GATED) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] *= acc[hx][1][i][q >> 2][q & 3] + b1[q];

@@ -195,7 +195,7 @@ __device__ __forceinline__ void up_group(const MoeArgs<E> &a, const E *const (&w
 #pragma unroll
             for (int v = 0; v < kWaves; ++v) z[m] += *reinterpret_cast<const f32x4 *>(red[v][m * TN + t][l]);
         float y[4] = {z[0][0], z[0][1], z[0][2], z[0][3]};
-        activate(y, a.act);
+        activate<sizeof(E) == 4>(y, a.act);
 #pragma unroll
         for (int q = 0; q < 4; ++q) a.H[(int64_t)pairs[at] * a.f + c + q] = to_elem<E>(y[q] * z[1][q]);
     }

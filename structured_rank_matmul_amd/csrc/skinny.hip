@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(LinearArgs<E, O> a)
         float y[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) y[q] = z[0][q] + (a.b0 && q < have ? to_f32(a.b0[c + q]) : 0.f);
-        activate(y, a.act);
+        activate<sizeof(O) == 4>(y, a.act);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (q >= have) continue;

@@ -186,7 +186,7 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
     if constexpr (sizeof(E) == 2) {
         const int64_t t256 = ((a.M + 255) / 256) * ((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-        if (t256 >= 128 && a.ldx <= (1 << 22) && a.ldw <= (1 << 22)) return launch_big<O, GATED>(a, st);
+        if (t256 >= 128 && big_strides(a)) return launch_big<O, GATED>(a, st);
     }
     const int64_t big = ((a.M + 127) / 128) * ((a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
     if (big >= 192) return launch_tile<E, O, 128, GATED ? 64 : 128, 2, 2, 2, GATED>(a, st);

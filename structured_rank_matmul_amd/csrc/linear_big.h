@@ -5,14 +5,12 @@
 // A workgroup owns 256 tokens and 256 weight rows (256 output features, or 128
 // gate and the same 128 up rows).  Wavefront (wm, wn) owns tokens 128 wm .. and
 // 64 weight rows: 128 accumulator registers.  K advances in slabs of 64 (128
-// bytes per row) through two LDS buffers.  A slab is four phases, one per
-// quadrant (token half x weight half) of the wavefront's block, 16 MFMAs each:
+// bytes per row) through two LDS buffers.  A slab is two phases, one per half of
+// the wavefront's tokens, 32 MFMAs each:
 //
-//     phase   reads into registers       product         copies
-//     0       tokens A (8 x 16 B)         A x weights A   tokens B of slab s + 1
-//     1       weights B (4)               A x weights B   weights A of slab s + 2
-//     2       tokens B (8)                B x weights B   tokens A of slab s + 2
-//     3       weights A of slab s + 1 (4) B x weights A   weights B of slab s + 2
+//     phase  reads into registers                    product            copies
+//     0      tokens A (8 x 16 B), weights B (4)       A x weights A, B   tokens B of slab s + 1, weights A of s + 2
+//     1      tokens B (8), weights A of s + 1 (4)     B x weights A, B   tokens A, weights B of slab s + 2
 //
 // The kernel is persistent and the copies run on through the end of a tile: the
 // last two slabs of a tile copy the first two of the workgroup's next one (of
@@ -21,21 +19,30 @@
 // of slab pairs; what lies past K is zero in LDS, by the buffer load's range
 // check.
 //
-// A phase is [reads, copies, wait] barrier [MFMAs] barrier, and the second
+// A phase is [reads, copies, waits] barrier [MFMAs] barrier, and the second
 // group (wm = 1, sharing each SIMD with the first) runs one barrier behind, so
-// that one group's MFMAs cover the other's reads.  A region of a buffer is
-// copied over two phases after its last read was issued: the read has then been
-// waited for by MFMAs that every wavefront finished a barrier before.  A copy
-// has five phases to land: each phase waits until at most 10 newer copies are
-// outstanding, and the barrier after it publishes them.  A wavefront's stores
-// count among its copies and complete in order with them; up to the first copy
-// issued after an epilogue, the waits leave that epilogue's stores outstanding
-// too (when their number is known: whole tiles, 16-byte stores).
+// that one group's 512 cycles of MFMAs cover the other's reads (about 400 at
+// 128 bytes a cycle).  Every read is waited for before the barrier that ends its
+// half of the phase, so a region may be copied over one phase after its last
+// read.  A copy has two phases (a slab) to land: each phase waits until at most
+// 8 newer copies are outstanding, and the barrier after it publishes them.  A
+// wavefront's stores count among its copies and complete in order with them; up
+// to the first copy issued after an epilogue, the waits leave that epilogue's
+// stores outstanding too (when their number is known: whole tiles, 16-byte
+// stores).
+//
+// Four phases of 16 MFMAs a slab, one per quadrant, took 811 us at 8192^3 where
+// two of 32 take 730 (1.51 PFLOP/s; the library's product 680).
 #pragma once
 
 #include "ffn_tile.h"
 
 namespace dyra {
+
+template <int N> __device__ __forceinline__ void wait_lds_and_vm() {
+    // lgkmcnt(0) and vmcnt(N): gfx9 encoding, expcnt left at its maximum
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
 
 template <int N> using ic = std::integral_constant<int, N>;
 
@@ -60,10 +67,10 @@ template <typename O, bool GATED>
 __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> a, int tiles_m, int tiles_n,
                                                             int per_xcd) {
     constexpr int BM = 256, BF = GATED ? 128 : 256;
-    constexpr int STAGE = 65536, WOFF = 32768;  // a buffer: 256 token rows, then 256 weight rows, of 128 bytes
+    constexpr int STAGE = 32768, WOFF = 65536;  // two buffers of 256 token rows of 128 bytes, two of 256 weight rows
     // 16-byte stores of a wavefront's epilogue
     constexpr int STORES = (GATED ? 1 : 2) * 8 * (8 * (int)sizeof(O) / 16);
-    __shared__ __align__(16) char smem[2 * STAGE];
+    __shared__ __align__(16) char smem[4 * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
@@ -145,7 +152,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
 
     f32x4 acc[2][2][4][2];  // [token half][weight half][token block][weight block]
     bf16x8 fx[2][4];        // [32-deep step][token block]
-    bf16x8 fw[2][2][2];     // [slot][step][weight block]
+    bf16x8 fw[3][2][2];     // [slot][step][weight block]
 
     const int swx = (i16 >> 1) & 7, sww = ((i16 >> 1) & 1) | ((i16 >> 2) << 1);
     const char *const px = smem + (128 * wm + i16) * 128;
@@ -166,46 +173,45 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
             for (int j = 0; j < 2; ++j)
                 fw[slot][k][j] = *reinterpret_cast<const bf16x8 *>(p + 4 * j * 128 + (((4 * k + g) ^ sww) << 4));
     };
-    auto products = [&](int hx, int hw, int slot) __attribute__((always_inline)) {
+    // 32 MFMAs: token half hx with both weight halves
+    auto products = [&](int hx, int slot_a, int slot_b) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         barrier_only();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int hw = 0; hw < 2; ++hw)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[hx][hw][i][j] = mma32(acc[hx][hw][i][j], fw[slot][k][j], fx[k][i]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[hx][hw][i][j] = mma32(acc[hx][hw][i][j], fw[hw ? slot_b : slot_a][k][j], fx[k][i]);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         barrier_only();
     };
     bool stores_out = false;  // the stores of the last epilogue may be left outstanding
     auto landed = [&](bool early) __attribute__((always_inline)) {
-        if (early) wait_vmcnt<10 + STORES>();
-        else wait_vmcnt<10>();
+        if (early) wait_lds_and_vm<8 + STORES>();
+        else wait_lds_and_vm<8>();
     };
-    // One slab in buffer B; slot B holds weights A, slot 1 - B is free.
+    // One slab in buffer B; slot B holds weights A.
     auto slab = [&](auto buffer, bool early) __attribute__((always_inline)) {
         constexpr int B = decltype(buffer)::value;
         read_x(0, B);
+        read_w(1, B, 2);
         copy_x(1, 1 - B);
-        landed(early);
-        products(0, 0, B);
         advance(B == 0);  // an even number of slabs: the copies change tiles in slab 0 of a pair
-        read_w(1, B, 1 - B);
         copy_w(0, B);
         landed(early && B == 0);
-        products(0, 1, 1 - B);
+        products(0, B, 2);
         read_x(1, B);
-        copy_x(0, B);
-        landed(early && B == 0);
-        products(1, 1, 1 - B);
         read_w(0, 1 - B, 1 - B);
+        copy_x(0, B);
         copy_w(1, B);
         landed(early && B == 0);
-        products(1, 0, B);
+        products(1, B, 2);
     };
 
     place(tile, row0, col0);
@@ -220,9 +226,11 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
     copy_w(0, 1);
     copy_x(0, 1);
     copy_w(1, 1);
-    wait_vmcnt<10>();
+    wait_vmcnt<8>();
     barrier_only();
     read_w(0, 0, 0);
+    wait_lds_and_vm<8>();
+    barrier_only();
     if (wm == 1) barrier_only();
     for (;;) {
 #pragma unroll
@@ -240,36 +248,42 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         // ---- epilogue: 8 consecutive features of a token per pair of weight blocks
         const int el = fresh_lane(), ei = el & 15, eg = el >> 4;
         stores_out = a.vec && row0 + BM <= a.M && col0 + BF <= a.N;
+        constexpr int HW = GATED ? 1 : 2;
+        int64_t c[HW];
+        int have[HW];
+        float b0[HW][8] = {}, b1[8] = {};
 #pragma unroll
-        for (int hw = 0; hw < (GATED ? 1 : 2); ++hw) {
-            const int64_t c = col0 + (GATED ? 32 * wn : 64 * wn + 32 * hw) + 8 * eg;
-            const int have = (int)min((int64_t)8, a.N - c);
-            if (have <= 0) continue;
-            float b0[8] = {}, b1[8] = {};
-            if (a.b0) load_row(a.b0 + c, b0, false, have);
-            if (GATED && a.b1) load_row(a.b1 + c, b1, false, have);
+        for (int hw = 0; hw < HW; ++hw) {
+            c[hw] = col0 + (GATED ? 32 * wn : 64 * wn + 32 * hw) + 8 * eg;
+            have[hw] = (int)min((int64_t)8, a.N - c[hw]);
+            if (a.b0) load_row(a.b0 + c[hw], b0[hw], false, have[hw]);
+            if (GATED && a.b1) load_row(a.b1 + c[hw], b1, false, have[hw]);
+        }
+        // both halves of a row one after the other: whole 128-byte lines
 #pragma unroll
-            for (int hx = 0; hx < 2; ++hx)
+        for (int hx = 0; hx < 2; ++hx)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t t = row0 + 128 * wm + 64 * hx + 16 * i + ei;
-                    if (t >= a.M) continue;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = row0 + 128 * wm + 64 * hx + 16 * i + ei;
+                if (t >= a.M) continue;
+#pragma unroll
+                for (int hw = 0; hw < HW; ++hw) {
                     float v[8];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = acc[hx][hw][i][q >> 2][q & 3] + b0[q];
+                    for (int q = 0; q < 8; ++q) v[q] = acc[hx][hw][i][q >> 2][q & 3] + b0[hw][q];
                     activate<sizeof(O) == 4>(v, a.act);
                     if constexpr (GATED) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) v[q] *= acc[hx][1][i][q >> 2][q & 3] + b1[q];
                     } else if (a.R) {
                         float r[8];
-                        load_row(a.R + t * a.ldr + c, r, a.vec, have);
+                        load_row(a.R + t * a.ldr + c[hw], r, a.vec, have[hw]);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) v[q] += r[q];
                     }
-                    store_row(a.Y + t * a.ldy + c, v, a.vec, have);
+                    store_row(a.Y + t * a.ldy + c[hw], v, a.vec, have[hw]);
                 }
-        }
+            }
         tile += nslots;
         if (tile >= band_end) break;
         row0 = next_row0;

@@ -331,7 +331,7 @@ typedef enum {
  *           they are.
  * dtype     DYRA_BF16 with out_dtype DYRA_BF16 or DYRA_F32, or DYRA_F32 with
  *           out_dtype DYRA_F32 (DYRA_ERR_DTYPE otherwise).
- * N >= 0 (0 is a no-op); N, c1, c2 <= 2^30.  X, Wt and their row strides are
+ * N >= 0 (0 is a no-op); N, c2 <= 2^30, c1, ldx, ldw <= 2^20.  X, Wt and their row strides are
  * 16-byte aligned, the others aligned to their elements (DYRA_ERR_ALIGN); a row
  * stride below the row's length is DYRA_ERR_ARG.
  */

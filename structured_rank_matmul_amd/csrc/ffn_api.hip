@@ -11,7 +11,10 @@ namespace {
 
 using dyra::bf16;
 
-constexpr int64_t kMaxDim = int64_t{1} << 30;  // tokens, features
+constexpr int64_t kMaxDim = int64_t{1} << 30;  // tokens, output features
+// Elements of a row of X or of a weight, and between rows: the kernels address
+// the rows of a tile by 32-bit byte offsets from its first.
+constexpr int64_t kMaxRow = int64_t{1} << 20;
 // Up to this many tokens the weights are streamed by skinny_kernel.
 constexpr int64_t kSkinnyTokens = 64;
 
@@ -29,7 +32,8 @@ dyra_status check_linear(const void *X, int64_t ldx, const void *W0, const void 
     *empty = false;
     if (!known(dtype) || !known(out) || (dtype == DYRA_F32 && out != DYRA_F32)) return DYRA_ERR_DTYPE;
     if (!known_act(act)) return DYRA_ERR_ARG;
-    if (N < 0 || c1 <= 0 || c2 <= 0 || N > kMaxDim || c1 > kMaxDim || c2 > kMaxDim) return DYRA_ERR_SHAPE;
+    if (N < 0 || c1 <= 0 || c2 <= 0 || N > kMaxDim || c2 > kMaxDim) return DYRA_ERR_SHAPE;
+    if (c1 > kMaxRow || ldx > kMaxRow || ldw > kMaxRow) return DYRA_ERR_SHAPE;
     const int64_t vec = 16 / (int64_t)size_of(dtype);
     if (c1 % vec != 0) return DYRA_ERR_SHAPE;
     if (ldx < c1 || ldw < c1 || ldy < c2) return DYRA_ERR_ARG;

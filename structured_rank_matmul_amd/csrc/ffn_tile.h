@@ -27,6 +27,19 @@ __device__ __forceinline__ f32x4 mma32(f32x4 acc, f32x8 a, f32x8 b) {
     return acc;
 }
 
+// A buffer resource over 2 GiB from `p` on; loads at kOutside and beyond give 0.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t panel(const void *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)(kOutside - 1), 0x00027000);
+}
+__device__ __forceinline__ void buffer_to_lds16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char *lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, (int)voff, (int)soff, 0, 0);
+}
+template <int N> __device__ __forceinline__ void wait_lds_and_vm() {
+    // lgkmcnt(0) and vmcnt(N): gfx9 encoding, expcnt left at its maximum
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
 // exp(v) and 1 / v by the hardware's exp2 and reciprocal (1 ulp each; the
 // product with log2(e) adds |v| u to the exponent's error).  The compiler's own
 // expf and division take about ten instructions each: at 25728 x 4096 outputs

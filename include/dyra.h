@@ -375,7 +375,8 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
  *
  *     Y[t] = residual[t] + sum_j weights[t][j] (act(X[t] Wg_e) * (X[t] Wu_e)) Wd_e,   e = ids[t][j]
  *
- * X         device, dtype, [T][c].  c and f whole numbers of 16-byte chunks.
+ * X         device, dtype, [T][c].  c and f whole numbers of 16-byte chunks;
+ *           c, f, ldx <= 2^18 (DYRA_ERR_SHAPE).
  * Wg, Wu    device, dtype, contiguous [experts][f][c];  Wd [experts][c][f].
  * ids       device int32 [T][topk]; a place whose id is not in [0, experts)
  *           adds nothing whatever its weight, an expert named twice counts twice.

@@ -15,6 +15,9 @@ constexpr int64_t kMaxDim = int64_t{1} << 30;  // tokens, output features
 // Elements of a row of X or of a weight, and between rows: the kernels address
 // the rows of a tile by 32-bit byte offsets from its first.
 constexpr int64_t kMaxRow = int64_t{1} << 20;
+// The same for the expert layer, whose pairs' rows (at most kMoeMaxPairs) are all
+// addressed from the first.
+constexpr int64_t kMaxExpertRow = int64_t{1} << 18;
 // Up to this many tokens the weights are streamed by skinny_kernel.
 constexpr int64_t kSkinnyTokens = 64;
 
@@ -114,7 +117,7 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
 }
 
 size_t dyra_moe_workspace_bytes(int64_t T, int32_t topk, int64_t f, dyra_dtype dtype) {
-    if (T < 0 || topk < 1 || f < 1 || f > kMaxDim || T > dyra::kMoeMaxPairs / topk || !known(dtype)) return 0;
+    if (T < 0 || topk < 1 || f < 1 || f > kMaxExpertRow || T > dyra::kMoeMaxPairs / topk || !known(dtype)) return 0;
     return (size_t)T * (size_t)topk * (size_t)f * size_of(dtype);
 }
 
@@ -125,7 +128,8 @@ dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f
     if (!known(dtype)) return DYRA_ERR_DTYPE;
     if (!known_act(act)) return DYRA_ERR_ARG;
     const int64_t vec = 16 / (int64_t)size_of(dtype);
-    if (T < 0 || c < 1 || f < 1 || c > kMaxDim || f > kMaxDim || c % vec != 0 || f % vec != 0) return DYRA_ERR_SHAPE;
+    if (T < 0 || c < 1 || f < 1 || c % vec != 0 || f % vec != 0) return DYRA_ERR_SHAPE;
+    if (c > kMaxExpertRow || f > kMaxExpertRow || ldx > kMaxExpertRow) return DYRA_ERR_SHAPE;
     if (experts < 1 || experts > dyra::kMoeMaxExperts || topk < 1 || topk > 64) return DYRA_ERR_SHAPE;
     if (T > dyra::kMoeMaxPairs / topk) return DYRA_ERR_SHAPE;
     if (ldx < c || ldy < c || (residual && ldr != 0 && ldr < c)) return DYRA_ERR_ARG;

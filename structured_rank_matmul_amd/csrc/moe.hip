@@ -6,9 +6,12 @@
 // Expert layer, two kernels.  moe_up forms H[pair][f] = act(X Wg_e^T) * (X Wu_e^T)
 // for every (token, place) pair; moe_down forms Y = R + sum_j w_j H_j Wd_e^T.
 // Both are bound by reading the weights of the chosen experts once: a workgroup
-// gathers the tokens of an expert and multiplies them together.  No atomics on
-// results: every pair's products have a place of their own in LDS and are added
-// per token in the order of its places.
+// gathers the tokens of an expert and multiplies them together, the weights
+// streamed through per-wavefront rings (skinny.h).  Every workgroup sorts the
+// places by expert itself (a few LDS steps), so that two launches do.  No
+// atomics on results: every pair's products have a place of their own in LDS and
+// are added per token in the order of its places.
+#include "lanes.h"
 #include "skinny.h"
 
 #include <algorithm>
@@ -103,169 +106,306 @@ __global__ __launch_bounds__(256) void route_kernel(const E *__restrict__ logits
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kDownPairs = 512;  // pairs of one moe_down workgroup
+constexpr int kSumStride = 20;   // floats of a token's 16 sums, padded
+constexpr int kDownPairs = 256;  // pairs of one moe_down workgroup
 
-// The pairs of the experts chosen by `n` places of ids, grouped by expert:
-// active expert a (in index order) is act[a], its pairs list[off[a] .. off[a+1]).
-template <int MAXP> struct ExpertLists {
-    int cursor[kMoeMaxExperts];
-    uint16_t act[kMoeMaxExperts];
-    uint16_t off[kMoeMaxExperts + 1];
-    uint16_t list[MAXP];
-    int n_act;
+// The places of ids grouped by expert, in order, and cut into slots of at most
+// SLOT pairs of one expert: slot s holds pairs list[first[s] .. + count[s]) of
+// expert[s].  Every workgroup builds the same ones.
+template <int MAXP, int SLOT> struct Slots {
+    uint16_t list[MAXP], expert[MAXP], first[MAXP], count[MAXP];
+    int n;
 
-    // All threads of the workgroup; ends with a barrier.  Places whose id is no
-    // expert are left out.  (The order of one expert's pairs may differ from run
-    // to run; each pair is a column of its own in every product, so no result
-    // depends on it.)
-    __device__ void build(const int32_t *ids, int n, int experts, int threads) {
+    // All kThreads threads; `cursor`: kMoeMaxExperts ints of LDS, `id`: MAXP more;
+    // ends with a barrier.  Places whose id is no expert are left out.
+    __device__ void build(const int32_t *ids, int places, int experts, int *cursor, int *id) {
         const int tid = threadIdx.x, lane = tid & 63;
-        for (int e = tid; e < experts; e += threads) cursor[e] = 0;
+        for (int e = tid; e < experts; e += kThreads) cursor[e] = 0;
         __syncthreads();
-        for (int p = tid; p < n; p += threads) {
+        for (int p = tid; p < places; p += kThreads) {
             const int e = ids[p];
-            if (e >= 0 && e < experts) atomicAdd(&cursor[e], 1);
+            id[p] = e >= 0 && e < experts ? e : -1;
+            if (id[p] >= 0) atomicAdd(&cursor[e], 1);
         }
         __syncthreads();
         if (tid < 64) {
-            int base = 0, na = 0;
+            int pairs = 0, slots = 0;
             for (int e0 = 0; e0 < experts; e0 += 64) {
                 const int e = e0 + lane;
-                const int c = e < experts ? cursor[e] : 0;
-                int incl = c;
+                const int c = e < experts ? cursor[e] : 0, s = (c + SLOT - 1) / SLOT;
+                int both = c | s << 16;  // prefix sums of pairs and slots (both below 2^15)
 #pragma unroll
                 for (int d = 1; d < 64; d <<= 1) {
-                    const int v = __shfl_up(incl, d);
-                    if (lane >= d) incl += v;
+                    const int v = __shfl_up(both, d);
+                    if (lane >= d) both += v;
                 }
-                const uint64_t m = __ballot(c > 0);
-                if (c > 0) {
-                    const int a = na + __popcll(m & ((uint64_t{1} << lane) - 1));
-                    act[a] = (uint16_t)e;
-                    off[a] = (uint16_t)(base + incl - c);
+                const int p0 = pairs + (both & 0xffff) - c, s0 = slots + (both >> 16) - s;
+                for (int q = 0; q < s; ++q) {
+                    expert[s0 + q] = (uint16_t)e;
+                    first[s0 + q] = (uint16_t)(p0 + SLOT * q);
+                    count[s0 + q] = (uint16_t)min(SLOT, c - SLOT * q);
                 }
-                if (e < experts) cursor[e] = base + incl - c;
-                base += __shfl(incl, 63);
-                na += __popcll(m);
+                if (e < experts) cursor[e] = p0;
+                const int last = __shfl(both, 63);
+                pairs += last & 0xffff;
+                slots += last >> 16;
             }
-            if (lane == 0) {
-                off[na] = (uint16_t)base;
-                n_act = na;
+            if (lane == 0) n = slots;
+            // 64 places at a time: a place's rank among those of its expert is the
+            // number of equal ids in the lanes below, found by one ballot per bit
+            const int bits = 32 - __clz(experts - 1 | 1);
+            for (int p0 = 0; p0 < places; p0 += 64) {
+                const int e = p0 + lane < places ? id[p0 + lane] : -1;
+                uint64_t same = __ballot(e >= 0);
+                for (int b = 0; b < bits; ++b) {
+                    const uint64_t set = __ballot(e >> b & 1);
+                    same &= e >> b & 1 ? set : ~set;
+                }
+                if (e >= 0) {
+                    const int rank = __popcll(same & ((uint64_t{1} << lane) - 1)), at = cursor[e];
+                    list[at + rank] = (uint16_t)(p0 + lane);
+                    if (rank == 0) cursor[e] = at + __popcll(same);
+                }
             }
-        }
-        __syncthreads();
-        for (int p = tid; p < n; p += threads) {
-            const int e = ids[p];
-            if (e >= 0 && e < experts) list[atomicAdd(&cursor[e], 1)] = (uint16_t)p;
         }
         __syncthreads();
     }
 };
 
-// One group of at most 16 TN pairs of an expert: partial sums of the
-// wavefronts' K ranges, joined in LDS, then H.
-template <typename E, int TN>
-__device__ __forceinline__ void up_group(const MoeArgs<E> &a, const E *const (&w)[2], const uint16_t *pairs, int n,
-                                         int64_t f0, float (*red)[4][64][4]) {
+// H = act(X Wg_e^T) * (X Wu_e^T) of every pair.  A unit is 8 gate and the same 8
+// up rows of one slot's expert; a workgroup takes a contiguous run of units
+// (slot by slot), its wavefronts split K and stream their parts through their
+// rings from unit to unit.  A slot's tokens stay in registers over its units
+// (two blocks of 16; SLABS slabs of K at a time, reloaded per unit where K has
+// more).
+template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs<E> a) {
+    constexpr int TB = 2;
+    __shared__ __align__(16) char ring_mem[kWaves * kRingBytes];
+    __shared__ __align__(16) float sums[TB][kWaves][16 * kSumStride];
+    __shared__ Slots<kMoeMaxPairs, 16 * TB> L;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int i16 = lane & 15, g = lane >> 4;
-    const E *x[TN];
-#pragma unroll
-    for (int t = 0; t < TN; ++t) {
-        const int p = pairs[std::min(16 * t + i16, n - 1)];
-        x[t] = a.X + (int64_t)(p / a.k) * a.ldx + 8 * g;
-    }
-    f32x4 acc[2][TN] = {};
-    const int steps = (int)((a.c + 31) / 32), per = (steps + kWaves - 1) / kWaves;
-    const int s0 = std::min(steps, wave * per), s1 = std::min(steps, s0 + per);
-    skinny_product<E, 2, TN, 4>(w, x, a.c, s0, s1, acc);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int t = 0; t < TN; ++t) *reinterpret_cast<f32x4 *>(red[wave][m * TN + t][lane]) = acc[m][t];
-    __syncthreads();
-    for (int u = tid; u < 64 * TN; u += kThreads) {
-        const int t = u / 64, l = u % 64, at = 16 * t + (l & 15);
-        const int64_t c = f0 + 4 * (l >> 4);
-        if (at >= n || c >= a.f) continue;
-        f32x4 z[2] = {};
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) z[m] += *reinterpret_cast<const f32x4 *>(red[v][m * TN + t][l]);
-        float y[4] = {z[0][0], z[0][1], z[0][2], z[0][3]};
-        activate<sizeof(E) == 4>(y, a.act);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) a.H[(int64_t)pairs[at] * a.f + c + q] = to_elem<E>(y[q] * z[1][q]);
-    }
-    __syncthreads();
-}
+    L.build(a.ids, a.T * a.k, a.experts, reinterpret_cast<int *>(ring_mem),
+            reinterpret_cast<int *>(ring_mem) + kMoeMaxExperts);
+    const int tiles = (int)((a.f + 7) / 8);
+    const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * tiles;
+    const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    if (u0 == u1) return;
 
-template <typename E> __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs<E> a) {
-    __shared__ ExpertLists<kMoeMaxPairs> L;
-    __shared__ float red[kWaves][4][64][4];
-    L.build(a.ids, a.T * a.k, a.experts, kThreads);
-    const int slot = (int)blockIdx.y;
-    if (slot >= L.n_act) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t f0 = (int64_t)blockIdx.x * 16;
-    const int64_t fr = std::min<int64_t>(f0 + (lane & 15), a.f - 1);
-    const int64_t row = ((int64_t)L.act[slot] * a.f + fr) * a.c + 8 * (lane >> 4);
-    const E *w[2] = {a.Wg + row, a.Wu + row};
-    for (int p = L.off[slot], e = L.off[slot + 1]; p < e;) {
-        if (e - p <= 16) {
-            up_group<E, 1>(a, w, L.list + p, e - p, f0, red);
-            p += 16;
-        } else {
-            up_group<E, 2>(a, w, L.list + p, std::min(32, e - p), f0, red);
-            p += 32;
+    const int row_bytes = (int)(a.c * (int)sizeof(E));
+    const int slabs = (row_bytes + 127) / 128, per = (slabs + kWaves - 1) / kWaves;
+    const int s0 = min(slabs, wave * per), s1 = min(slabs, s0 + per);
+
+    SlabRows w;
+    SlabRing<E, false> ring{ring_mem + wave * kRingBytes};
+    int in_slot = u0 / tiles, in_tile = u0 % tiles, in_left = u1 - u0, in_slab = s0;
+    auto aim = [&]() __attribute__((always_inline)) {
+        const int e = __builtin_amdgcn_readfirstlane(L.expert[in_slot]);
+        const int64_t row = (int64_t)e * a.f + 8 * (int64_t)in_tile;
+        w.buf[0] = panel(a.Wg + row * a.c);
+        w.buf[1] = panel(a.Wu + row * a.c);
+        const int last = (int)min((int64_t)8, a.f - 8 * (int64_t)in_tile) - 1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) w.off[q] = (uint32_t)min(slab_row(q) & 7, last) * (uint32_t)row_bytes + slab_chunk(q);
+    };
+    aim();
+    auto ahead = [&]() __attribute__((always_inline)) {
+        if (in_left == 0 || s0 == s1) return;
+        ring.issue(w, w, 128u * (uint32_t)in_slab, row_bytes - 128 * in_slab);
+        if (++in_slab == s1) {
+            in_slab = s0;
+            if (++in_tile == tiles) {
+                in_tile = 0;
+                ++in_slot;
+            }
+            if (--in_left > 0) aim();
+        }
+    };
+
+    SlabFrag<E> x[TB][SLABS];
+    const __amdgpu_buffer_rsrc_t xbuf = panel(a.X);
+    auto load_tokens = [&](int slot, int s) __attribute__((always_inline)) {
+        const int n = L.count[slot];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const int at = 16 * t + (lane & 15);
+            uint32_t row = kOutside;
+            if (at < n) row = (uint32_t)(L.list[L.first[slot] + at] / a.k) * (uint32_t)(a.ldx * sizeof(E));
+#pragma unroll
+            for (int j = 0; j < SLABS; ++j)
+                x[t][j] = slab_load<E>(xbuf, row, 128u * (uint32_t)(s + j), at < n ? row_bytes - 128 * (s + j) : 0);
+        }
+    };
+    int slot = u0 / tiles, tile = u0 % tiles, first = 0;
+    load_tokens(slot, s0);
+    asm volatile("" ::: "memory");
+#pragma unroll 1
+    for (int p = 0; p < ring.DEPTH; ++p) ahead();
+    bool fresh = true;  // x holds this slot's first slabs
+    for (int u = u0; u < u1; ++u) {
+        f32x4 acc[TB] = {};
+        for (int s = s0; s < s1; s += SLABS) {
+            if (!fresh) load_tokens(slot, s);
+            fresh = per <= SLABS;
+            unroll_seq<SLABS>([&](auto j) __attribute__((always_inline)) {
+                if (s + (int)j >= s1) return;
+                SlabFrag<E> fw, unused;
+                ring.take(fw, unused);
+                ahead();
+#pragma unroll
+                for (int t = 0; t < TB; ++t) acc[t] = slab_product(acc[t], fw, x[t][j]);
+            });
+        }
+        __syncthreads();  // the last unit's sums have been read
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            *reinterpret_cast<f32x4 *>(&sums[t][wave][(lane & 15) * kSumStride + 4 * (lane >> 4)]) = acc[t];
+        __syncthreads();
+        // 8 features of up to 32 pairs, by four of the wavefronts in turn
+        const int th = (tid - first) & (kThreads - 1), q = th & 7, at = th >> 3;
+        first += 256;
+        const int64_t c = 8 * (int64_t)tile + q;
+        if (at < L.count[slot] && c < a.f) {
+            const int t = at >> 4, i = at & 15;
+            float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) {
+                z0 += sums[t][v][i * kSumStride + q];
+                z1 += sums[t][v][i * kSumStride + 8 + q];
+            }
+            float y[1] = {z0};
+            activate<sizeof(E) == 4>(y, a.act);
+            a.H[(int64_t)L.list[L.first[slot] + at] * a.f + c] = to_elem<E>(y[0] * z1);
+        }
+        if (++tile == tiles) {
+            tile = 0;
+            ++slot;
+            fresh = false;
         }
     }
 }
 
-// A workgroup owns 16 output features of a chunk of tokens.  Its wavefronts
-// take (expert, part of f) units; the products of a pair go to the pair's own
-// place of P, and the places of a token are added at the end in order.
-template <typename E> __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk, int parts) {
-    __shared__ ExpertLists<kDownPairs> L;
-    extern __shared__ __align__(16) float P[];  // [parts][chunk k][16]
+// Y = R + sum_j w_j H_j Wd_e^T.  A workgroup owns ROWS output features of a chunk
+// of tokens.  The slabs of f of all its slots, one slot after the other, are
+// dealt to its wavefronts in eight equal runs; a wavefront streams the weights'
+// and the pairs' slabs of its run through its ring and keeps one slot's sums at a
+// time.  A run's sums of a slot go to the pairs' own places in LDS, except
+// those of a first slot that the run before began: these go to the wavefront's
+// own place and are added afterwards in the order of the wavefronts.  At the end
+// each token's places are added in order.
+template <typename E, int ROWS> __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk) {
+    __shared__ __align__(16) char ring_mem[kWaves * kRingBytes];
+    __shared__ __align__(16) float P[kDownPairs * ROWS];
+    __shared__ __align__(16) float head[kWaves][16 * ROWS];
+    __shared__ Slots<kDownPairs, 16> L;
+    __shared__ float weight[kDownPairs];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i16 = lane & 15, g = lane >> 4;
-    const int t0 = (int)blockIdx.y * chunk, tn = std::min(chunk, a.T - t0);
-    const int np = chunk * a.k;
-    const int64_t c0 = (int64_t)blockIdx.x * 16;
-    L.build(a.ids + (int64_t)t0 * a.k, tn * a.k, a.experts, kThreads);
-    const int steps = (int)((a.f + 31) / 32), per = (steps + parts - 1) / parts;
-    const int64_t cr = std::min<int64_t>(c0 + i16, a.c - 1);
-    for (int u = wave; u < L.n_act * parts; u += kWaves) {
-        const int s = u / parts, part = u % parts;
-        const int s0 = std::min(steps, part * per), s1 = std::min(steps, s0 + per);
-        const E *w[1] = {a.Wd + ((int64_t)L.act[s] * a.c + cr) * a.f + 8 * g};
-        for (int p = L.off[s], e = L.off[s + 1]; p < e; p += 16) {
-            const int pair = L.list[std::min(p + i16, e - 1)];
-            const E *x[1] = {a.H + ((int64_t)t0 * a.k + pair) * a.f + 8 * g};
-            f32x4 acc[1][1] = {};
-            skinny_product<E, 1, 1, 8>(w, x, a.f, s0, s1, acc);
-            if (p + i16 < e) *reinterpret_cast<f32x4 *>(P + ((int64_t)part * np + pair) * 16 + 4 * g) = acc[0][0];
+    const int t0 = (int)blockIdx.y * chunk, tn = min(chunk, a.T - t0), places = tn * a.k;
+    const int64_t c0 = (int64_t)blockIdx.x * ROWS;
+    const int32_t *ids = a.ids + (int64_t)t0 * a.k;
+    for (int p = tid; p < places; p += kThreads) {
+        const int e = ids[p];
+        const bool chosen = e >= 0 && e < a.experts;
+        weight[p] = chosen ? a.w[(int64_t)t0 * a.k + p] : 0.f;
+        if (!chosen) {  // adds 0
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) P[p * ROWS + q] = 0.f;
+        }
+    }
+    L.build(ids, places, a.experts, reinterpret_cast<int *>(ring_mem),
+            reinterpret_cast<int *>(ring_mem) + kMoeMaxExperts);
+    const int row_bytes = (int)(a.f * (int)sizeof(E));
+    const int slabs = (row_bytes + 127) / 128;
+    const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * slabs;
+    auto run_start = [&](int v) { return total * v / kWaves; };
+    const int64_t r0 = run_start(wave), r1 = run_start(wave + 1);
+
+    SlabRows w, x;
+    SlabRing<E, true, ROWS> ring{ring_mem + wave * kRingBytes};
+    int64_t in_left = r1 - r0;
+    int in_slot = (int)(r0 / slabs), in_slab = (int)(r0 % slabs);
+    x.buf[0] = x.buf[1] = panel(a.H + (int64_t)t0 * a.k * a.f);
+    auto aim = [&]() __attribute__((always_inline)) {
+        const int e = __builtin_amdgcn_readfirstlane(L.expert[in_slot]);
+        w.buf[0] = w.buf[1] = panel(a.Wd + ((int64_t)e * a.c + c0) * a.f);
+        const int last = (int)min((int64_t)ROWS, a.c - c0) - 1, n = L.count[in_slot], f0 = L.first[in_slot];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            w.off[q] = (uint32_t)min(slab_row(q), last) * (uint32_t)row_bytes + slab_chunk(q);
+            // rows past the slot's pairs read nothing
+            x.off[q] = slab_row(q) < n ? (uint32_t)L.list[f0 + slab_row(q)] * (uint32_t)row_bytes + slab_chunk(q) : kOutside;
+        }
+    };
+    auto ahead = [&]() __attribute__((always_inline)) {
+        if (in_left == 0) return;
+        ring.issue(w, x, 128u * (uint32_t)in_slab, row_bytes - 128 * in_slab);
+        --in_left;
+        if (++in_slab == slabs) {
+            in_slab = 0;
+            ++in_slot;
+            if (in_left > 0) aim();
+        }
+    };
+    if (in_left > 0) aim();
+#pragma unroll 1
+    for (int p = 0; p < ring.DEPTH; ++p) ahead();
+
+    int slot = (int)(r0 / slabs), slab = (int)(r0 % slabs);
+    bool begun = slab != 0;  // by the run before
+    f32x4 acc = {};
+#pragma unroll 1
+    for (int64_t r = r0; r < r1; ++r) {
+        SlabFrag<E> fw, fx;
+        ring.take(fw, fx);
+        ahead();
+        acc = slab_product(acc, fw, fx);
+        if (++slab == slabs || r + 1 == r1) {
+            if (4 * g < ROWS) {
+                if (begun) *reinterpret_cast<f32x4 *>(&head[wave][i16 * ROWS + 4 * g]) = acc;
+                else if (i16 < L.count[slot])
+                    *reinterpret_cast<f32x4 *>(&P[L.list[L.first[slot] + i16] * ROWS + 4 * g]) = acc;
+            }
+            acc = f32x4{};
+            begun = false;
+            slab = 0;
+            ++slot;
         }
     }
     __syncthreads();
-    for (int u = tid; u < tn * 16; u += kThreads) {
-        const int t = u / 16, q = u % 16;
+    if (tid < 16 * ROWS) {  // this thread's column and row of every slot that a run continued
+        const int i = tid / ROWS, q = tid % ROWS;
+        for (int v = 1; v < kWaves; ++v) {
+            const int64_t b = run_start(v);
+            const int s = (int)(b / slabs);
+            if (b < run_start(v + 1) && b % slabs != 0 && i < L.count[s])
+                P[L.list[L.first[s] + i] * ROWS + q] += head[v][i * ROWS + q];
+        }
+    }
+    __syncthreads();
+    for (int u = tid; u < tn * ROWS; u += kThreads) {
+        const int t = u / ROWS, q = u % ROWS;
         const int64_t tok = t0 + t;
         if (c0 + q >= a.c) continue;
-        float y = a.R ? to_f32(a.R[tok * a.ldr + c0 + q]) : 0.f, sum = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            const int e = a.ids[tok * a.k + j];
-            if (e < 0 || e >= a.experts) continue;
-            float o = 0.f;
-            for (int s = 0; s < parts; ++s) o += P[((int64_t)s * np + t * a.k + j) * 16 + q];
-            sum += a.w[tok * a.k + j] * o;
-        }
-        a.Y[tok * a.ldy + c0 + q] = to_elem<E>(sum + y);
+        float sum = 0.f;
+        for (int j = 0; j < a.k; ++j) sum += weight[t * a.k + j] * P[(t * a.k + j) * ROWS + q];
+        if (a.R) sum += to_f32(a.R[tok * a.ldr + c0 + q]);
+        a.Y[tok * a.ldy + c0 + q] = to_elem<E>(sum);
     }
+}
+
+template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipStream_t st) {
+    const int64_t most = (int64_t)std::min(a.T * a.k, a.experts + a.T * a.k / 32) * ((a.f + 7) / 8);  // units
+    hipLaunchKernelGGL((moe_up_kernel<E, SLABS>), dim3((unsigned)std::min<int64_t>(most, 256)), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+}
+template <typename E, int ROWS> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
+    const int chunk = std::min(a.T, kDownPairs / a.k);
+    hipLaunchKernelGGL((moe_down_kernel<E, ROWS>),
+                       dim3((unsigned)((a.c + ROWS - 1) / ROWS), (unsigned)((a.T + chunk - 1) / chunk)), dim3(kThreads),
+                       0, st, a, chunk);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -292,18 +432,14 @@ template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st)
     if (a.T <= 0) return hipSuccess;
     const int pairs = a.T * a.k;
     if (pairs > kMoeMaxPairs || a.experts > kMoeMaxExperts) return hipErrorInvalidValue;
-    const int slots = std::min(a.experts, pairs);
-    hipLaunchKernelGGL((moe_up_kernel<E>), dim3((unsigned)((a.f + 15) / 16), (unsigned)slots), dim3(kThreads), 0, st, a);
-    hipError_t e = hipGetLastError();
+    const int slabs = (int)((a.c * (int64_t)sizeof(E) + 128 * kWaves - 1) / (128 * kWaves));  // of K, a wavefront's
+    const hipError_t e = slabs <= 2   ? launch_up<E, 2>(a, st)
+                         : slabs <= 4 ? launch_up<E, 4>(a, st)
+                         : slabs <= 8 ? launch_up<E, 8>(a, st)
+                                      : launch_up<E, 12>(a, st);
     if (e != hipSuccess) return e;
-    const int chunk = std::min(a.T, kDownPairs / a.k);
-    // units enough for two rounds of the wavefronts, within 32 KB of partial sums
-    const int parts = std::max(1, std::min({(2 * kWaves + slots - 1) / slots, kDownPairs / (chunk * a.k),
-                                            (int)((a.f + 255) / 256)}));
-    hipLaunchKernelGGL((moe_down_kernel<E>),
-                       dim3((unsigned)((a.c + 15) / 16), (unsigned)((a.T + chunk - 1) / chunk)), dim3(kThreads),
-                       sizeof(float) * (size_t)parts * chunk * a.k * 16, st, a, chunk, parts);
-    return hipGetLastError();
+    // 8 rows a workgroup where 16 would leave CUs without one
+    return a.c <= 16 * 255 ? launch_down<E, 8>(a, st) : launch_down<E, 16>(a, st);
 }
 
 template hipError_t launch_route<float>(const float *, int64_t, int64_t, int, int, bool, bool, float, int32_t *, float *,

@@ -42,10 +42,10 @@ __device__ __forceinline__ f32x4 slab_product(f32x4 acc, const SlabFrag<bf16> &w
 __device__ __forceinline__ f32x4 slab_product(f32x4 acc, const SlabFrag<float> &w, const SlabFrag<float> &x) {
     return mma32(acc, w.f[0], x.f[0]);
 }
-// The fragments of row `lane % 16` of a slab in LDS.
-template <typename E> __device__ __forceinline__ SlabFrag<E> slab_read(const char *slab) {
-    const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4, sw = i16 >> 1;
-    const char *p = slab + i16 * 128;
+// The fragments of row `lane % ROWS` of a slab in LDS.
+template <typename E, int ROWS> __device__ __forceinline__ SlabFrag<E> slab_read(const char *slab) {
+    const int lane = threadIdx.x & 63, r16 = lane & (ROWS - 1), g = lane >> 4, sw = r16 >> 1;
+    const char *p = slab + r16 * 128;
     SlabFrag<E> r;
     if constexpr (sizeof(E) == 2) {
 #pragma unroll
@@ -64,6 +64,7 @@ template <typename E> __device__ __forceinline__ SlabFrag<E> slab_load(__amdgpu_
     const uint32_t g = (threadIdx.x & 63) >> 4;
     SlabFrag<E> r;
     auto chunk = [&](uint32_t c) -> u32x4 {
+        // (a row at kOutside stays outside: zeros)
         return __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(16 * c) < left ? row + 16 * c : kOutside, (int)k, 0);
     };
     if constexpr (sizeof(E) == 2) {
@@ -79,92 +80,42 @@ template <typename E> __device__ __forceinline__ SlabFrag<E> slab_load(__amdgpu_
 constexpr int kRingBytes = 16384;  // of LDS for each wavefront's ring
 
 // One wavefront's ring of slabs: of weights, or (TOKENS) of weights and tokens.
-template <typename E, bool TOKENS> struct SlabRing {
-    static constexpr int SLAB = TOKENS ? 4096 : 2048, DEPTH = kRingBytes / SLAB, COPIES = TOKENS ? 4 : 2;
+// WROWS: 16 weight rows a slab, or 8 (rows 8 .. 15 of the fragments repeat them).
+template <typename E, bool TOKENS, int WROWS = 16> struct SlabRing {
+    static constexpr int WBYTES = 128 * WROWS, SLAB = WBYTES + (TOKENS ? 2048 : 0);
+    static constexpr int DEPTH = kRingBytes / SLAB, COPIES = WROWS / 8 + (TOKENS ? 2 : 0);
     char *ring;            // this wavefront's kRingBytes of LDS
-    int put = 0, got = 0;  // slabs issued and consumed
+    int ahead = 0;             // slabs issued and not consumed
+    int put = 0, got = 0;      // places of the next slab to issue and to consume
 
-    __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
+    template <int ROWS> __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < ROWS / 8; ++q)
             buffer_to_lds16(r.buf[q], (int)slab_chunk(q) < left ? r.off[q] : kOutside, k, dst + 1024 * q);
     }
     // Copies one slab at byte `k` of the rows; `left` bytes of the rows are left.
     __device__ __forceinline__ void issue(const SlabRows &w, const SlabRows &x, uint32_t k, int left) {
-        char *dst = ring + (put % DEPTH) * SLAB;
-        copy(w, k, left, dst);
-        if constexpr (TOKENS) copy(x, k, left, dst + 2048);
-        ++put;
+        char *dst = ring + put * SLAB;
+        copy<WROWS>(w, k, left, dst);
+        if constexpr (TOKENS) copy<16>(x, k, left, dst + WBYTES);
+        put = put + 1 == DEPTH ? 0 : put + 1;
+        ++ahead;
     }
     // Waits for the oldest slab and reads its fragments; its place is then free.
     __device__ __forceinline__ void take(SlabFrag<E> &w, SlabFrag<E> &x) {
         // (stores issued in between only make the wait stricter)
-        if (put - got == DEPTH) wait_vmcnt<(DEPTH - 1) * COPIES>();
+        if (ahead == DEPTH) wait_vmcnt<(DEPTH - 1) * COPIES>();
         else wait_vmcnt<0>();
         // the copies write LDS behind the compiler's back: no read may move above the wait
         asm volatile("" ::: "memory");
-        const char *slab = ring + (got % DEPTH) * SLAB;
-        w = slab_read<E>(slab);
-        if constexpr (TOKENS) x = slab_read<E>(slab + 2048);
+        const char *slab = ring + got * SLAB;
+        w = slab_read<E, WROWS>(slab);
+        if constexpr (TOKENS) x = slab_read<E, 16>(slab + WBYTES);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the fragments are in registers
         asm volatile("" ::: "memory");
-        ++got;
+        got = got + 1 == DEPTH ? 0 : got + 1;
+        --ahead;
     }
 };
-
-__device__ __align__(16) static const unsigned g_skinny_zero[4] = {0, 0, 0, 0};
-
-// This lane's 8 elements of a 32-deep step: p points at element 8 (lane / 16)
-// of the step and `left` elements of the row are left from there on.
-__device__ __forceinline__ bf16x8 step_frag(const bf16 *p) { return *reinterpret_cast<const bf16x8 *>(p); }
-__device__ __forceinline__ f32x8 step_frag(const float *p) { return ld_frag(p); }
-__device__ __forceinline__ bf16x8 step_frag_tail(const bf16 *p, int64_t left) {
-    return *reinterpret_cast<const bf16x8 *>(left > 0 ? (const void *)p : (const void *)g_skinny_zero);
-}
-__device__ __forceinline__ f32x8 step_frag_tail(const float *p, int64_t left) {
-    const f32x4 lo = *reinterpret_cast<const f32x4 *>(left > 0 ? (const void *)p : (const void *)g_skinny_zero);
-    const f32x4 hi = *reinterpret_cast<const f32x4 *>(left > 4 ? (const void *)(p + 4) : (const void *)g_skinny_zero);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// acc[m][t] += W_m[16 rows] X_t[16 tokens]^T over steps [s0, s1) of 32.
-// w[m], x[t]: this lane's row pointers, already at element 8 (lane / 16).
-template <typename E, int MATS, int TN, int UNROLL>
-__device__ __forceinline__ void skinny_product(const E *const (&w)[MATS], const E *const (&x)[TN], int64_t K, int s0,
-                                               int s1, f32x4 (&acc)[MATS][TN]) {
-    typedef typename Frag<E>::type F;
-    const int g = (threadIdx.x & 63) >> 4;
-    const int whole = (int)(K / 32);  // steps with every element
-    int s = s0;
-    const int e = s1 < whole ? s1 : whole;
-    for (; s + UNROLL <= e; s += UNROLL) {
-        F fw[UNROLL][MATS], fx[UNROLL][TN];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-#pragma unroll
-            for (int m = 0; m < MATS; ++m) fw[u][m] = step_frag(w[m] + (int64_t)(s + u) * 32);
-#pragma unroll
-            for (int t = 0; t < TN; ++t) fx[u][t] = step_frag(x[t] + (int64_t)(s + u) * 32);
-        }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-            for (int m = 0; m < MATS; ++m)
-#pragma unroll
-                for (int t = 0; t < TN; ++t) acc[m][t] = mma32(acc[m][t], fw[u][m], fx[u][t]);
-    }
-    for (; s < s1; ++s) {
-        const int64_t left = K - (int64_t)s * 32 - 8 * g;
-        F fw[MATS], fx[TN];
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) fw[m] = step_frag_tail(w[m] + (int64_t)s * 32, left);
-#pragma unroll
-        for (int t = 0; t < TN; ++t) fx[t] = step_frag_tail(x[t] + (int64_t)s * 32, left);
-#pragma unroll
-        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-            for (int t = 0; t < TN; ++t) acc[m][t] = mma32(acc[m][t], fw[m], fx[t]);
-    }
-}
 
 }  // namespace dyra

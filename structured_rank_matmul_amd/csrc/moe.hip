@@ -104,10 +104,8 @@ __global__ __launch_bounds__(256) void route_kernel(const E *__restrict__ logits
 
 // ------------------------------------------------------------------ expert layer
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kSumStride = 20;   // floats of a token's 16 sums, padded
-constexpr int kDownPairs = 256;  // pairs of one moe_down workgroup
+// Pairs of one moe_down workgroup: 16 KB of sums.
+template <int ROWS> constexpr int kDownPairs = 4096 / ROWS;
 
 // The places of ids grouped by expert, in order, and cut into slots of at most
 // SLOT pairs of one expert: slot s holds pairs list[first[s] .. + count[s]) of
@@ -116,9 +114,10 @@ template <int MAXP, int SLOT> struct Slots {
     uint16_t list[MAXP], expert[MAXP], first[MAXP], count[MAXP];
     int n;
 
-    // All kThreads threads; `cursor`: kMoeMaxExperts ints of LDS, `id`: MAXP more;
-    // ends with a barrier.  Places whose id is no expert are left out.
-    __device__ void build(const int32_t *ids, int places, int experts, int *cursor, int *id) {
+    // All kThreads threads; `scratch`: kMoeMaxExperts + MAXP ints of LDS; ends with
+    // a barrier.  Places whose id is no expert are left out.
+    __device__ void build(const int32_t *ids, int places, int experts, int *scratch) {
+        int *const cursor = scratch, *const id = scratch + kMoeMaxExperts;
         const int tid = threadIdx.x, lane = tid & 63;
         for (int e = tid; e < experts; e += kThreads) cursor[e] = 0;
         __syncthreads();
@@ -173,116 +172,69 @@ template <int MAXP, int SLOT> struct Slots {
 };
 
 // H = act(X Wg_e^T) * (X Wu_e^T) of every pair.  A unit is 8 gate and the same 8
-// up rows of one slot's expert; a workgroup takes a contiguous run of units
-// (slot by slot), its wavefronts split K and stream their parts through their
-// rings from unit to unit.  A slot's tokens stay in registers over its units
-// (two blocks of 16; SLABS slabs of K at a time, reloaded per unit where K has
-// more).
-template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs<E> a) {
-    constexpr int TB = 2;
-    __shared__ __align__(16) char ring_mem[kWaves * kRingBytes];
-    __shared__ __align__(16) float sums[TB][kWaves][16 * kSumStride];
-    __shared__ Slots<kMoeMaxPairs, 16 * TB> L;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    L.build(a.ids, a.T * a.k, a.experts, reinterpret_cast<int *>(ring_mem),
-            reinterpret_cast<int *>(ring_mem) + kMoeMaxExperts);
-    const int tiles = (int)((a.f + 7) / 8);
-    const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * tiles;
-    const int u0 = (int)(total * blockIdx.x / gridDim.x), u1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-    if (u0 == u1) return;
-
-    const int row_bytes = (int)(a.c * (int)sizeof(E));
-    const int slabs = (row_bytes + 127) / 128, per = (slabs + kWaves - 1) / kWaves;
-    const int s0 = min(slabs, wave * per), s1 = min(slabs, s0 + per);
-
-    SlabRows w;
-    SlabRing<E, false> ring{ring_mem + wave * kRingBytes};
-    int in_slot = u0 / tiles, in_tile = u0 % tiles, in_left = u1 - u0, in_slab = s0;
-    auto aim = [&]() __attribute__((always_inline)) {
-        const int e = __builtin_amdgcn_readfirstlane(L.expert[in_slot]);
-        const int64_t row = (int64_t)e * a.f + 8 * (int64_t)in_tile;
+// up rows of one slot's expert; a workgroup takes a contiguous run of units, slot
+// by slot, so that a slot's tokens stay in registers over its units.
+constexpr int kUpSlot = 32;
+struct UpLds {
+    StreamLds<2> stream;
+    Slots<kMoeMaxPairs, kUpSlot> slots;
+};
+template <typename E> struct UpPositions {
+    static constexpr int kFinishers = 8 * kUpSlot;
+    const MoeArgs<E> &a;
+    const Slots<kMoeMaxPairs, kUpSlot> &L;
+    int tiles, u0, count;
+    __device__ UpPositions(const MoeArgs<E> &args, const Slots<kMoeMaxPairs, kUpSlot> &slots) : a(args), L(slots) {
+        tiles = (int)((a.f + 7) / 8);
+        const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * tiles;
+        u0 = (int)(total * blockIdx.x / gridDim.x);
+        count = (int)(total * (blockIdx.x + 1) / gridDim.x) - u0;
+    }
+    __device__ __forceinline__ int slot(int p) const { return (u0 + p) / tiles; }
+    __device__ __forceinline__ int tile(int p) const { return (u0 + p) % tiles; }
+    __device__ __forceinline__ int pairs(int p) const { return __builtin_amdgcn_readfirstlane(L.count[slot(p)]); }
+    __device__ __forceinline__ void weights(int p, SlabRows &w) const {
+        const int e = __builtin_amdgcn_readfirstlane(L.expert[slot(p)]), t = tile(p);
+        const int64_t row = (int64_t)e * a.f + 8 * (int64_t)t;
         w.buf[0] = panel(a.Wg + row * a.c);
         w.buf[1] = panel(a.Wu + row * a.c);
-        const int last = (int)min((int64_t)8, a.f - 8 * (int64_t)in_tile) - 1;
+        const int last = (int)min((int64_t)8, a.f - 8 * (int64_t)t) - 1;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w.off[q] = (uint32_t)min(slab_row(q) & 7, last) * (uint32_t)row_bytes + slab_chunk(q);
-    };
-    aim();
-    auto ahead = [&]() __attribute__((always_inline)) {
-        if (in_left == 0 || s0 == s1) return;
-        ring.issue(w, w, 128u * (uint32_t)in_slab, row_bytes - 128 * in_slab);
-        if (++in_slab == s1) {
-            in_slab = s0;
-            if (++in_tile == tiles) {
-                in_tile = 0;
-                ++in_slot;
+        for (int q = 0; q < 2; ++q)
+            w.off[q] = (uint32_t)min(slab_row(q) & 7, last) * (uint32_t)(a.c * sizeof(E)) + slab_chunk(q);
+    }
+    __device__ __forceinline__ bool new_tokens(int p) const { return p == 0 || tile(p) == 0; }
+    __device__ __forceinline__ int blocks(int p) const { return pairs(p) > 16 ? 2 : 1; }
+    __device__ __forceinline__ void tokens(int p, SlabRows (&x)[2]) const {
+        const int n = pairs(p), first = L.first[slot(p)];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            x[t].buf[0] = x[t].buf[1] = panel(a.X);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // rows past the slot's pairs read nothing
+                const int at = 16 * t + slab_row(q);
+                x[t].off[q] = kOutside;
+                if (at < n)
+                    x[t].off[q] = (uint32_t)(L.list[first + at] / a.k) * (uint32_t)(a.ldx * sizeof(E)) + slab_chunk(q);
             }
-            if (--in_left > 0) aim();
-        }
-    };
-
-    SlabFrag<E> x[TB][SLABS];
-    const __amdgpu_buffer_rsrc_t xbuf = panel(a.X);
-    auto load_tokens = [&](int slot, int s) __attribute__((always_inline)) {
-        const int n = L.count[slot];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const int at = 16 * t + (lane & 15);
-            uint32_t row = kOutside;
-            if (at < n) row = (uint32_t)(L.list[L.first[slot] + at] / a.k) * (uint32_t)(a.ldx * sizeof(E));
-#pragma unroll
-            for (int j = 0; j < SLABS; ++j)
-                x[t][j] = slab_load<E>(xbuf, row, 128u * (uint32_t)(s + j), at < n ? row_bytes - 128 * (s + j) : 0);
-        }
-    };
-    int slot = u0 / tiles, tile = u0 % tiles, first = 0;
-    load_tokens(slot, s0);
-    asm volatile("" ::: "memory");
-#pragma unroll 1
-    for (int p = 0; p < ring.DEPTH; ++p) ahead();
-    bool fresh = true;  // x holds this slot's first slabs
-    for (int u = u0; u < u1; ++u) {
-        f32x4 acc[TB] = {};
-        for (int s = s0; s < s1; s += SLABS) {
-            if (!fresh) load_tokens(slot, s);
-            fresh = per <= SLABS;
-            unroll_seq<SLABS>([&](auto j) __attribute__((always_inline)) {
-                if (s + (int)j >= s1) return;
-                SlabFrag<E> fw, unused;
-                ring.take(fw, unused);
-                ahead();
-#pragma unroll
-                for (int t = 0; t < TB; ++t) acc[t] = slab_product(acc[t], fw, x[t][j]);
-            });
-        }
-        __syncthreads();  // the last unit's sums have been read
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-            *reinterpret_cast<f32x4 *>(&sums[t][wave][(lane & 15) * kSumStride + 4 * (lane >> 4)]) = acc[t];
-        __syncthreads();
-        // 8 features of up to 32 pairs, by four of the wavefronts in turn
-        const int th = (tid - first) & (kThreads - 1), q = th & 7, at = th >> 3;
-        first += 256;
-        const int64_t c = 8 * (int64_t)tile + q;
-        if (at < L.count[slot] && c < a.f) {
-            const int t = at >> 4, i = at & 15;
-            float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) {
-                z0 += sums[t][v][i * kSumStride + q];
-                z1 += sums[t][v][i * kSumStride + 8 + q];
-            }
-            float y[1] = {z0};
-            activate<sizeof(E) == 4>(y, a.act);
-            a.H[(int64_t)L.list[L.first[slot] + at] * a.f + c] = to_elem<E>(y[0] * z1);
-        }
-        if (++tile == tiles) {
-            tile = 0;
-            ++slot;
-            fresh = false;
         }
     }
+    __device__ __forceinline__ void finish(int p, const float *sums, int thread) const {
+        const int q = thread & 7, at = thread >> 3;
+        const int64_t c = 8 * (int64_t)tile(p) + q;
+        if (at >= pairs(p) || c >= a.f) return;
+        const float *block = sums + (at >> 4) * kWaves * kBlockSums;
+        float y[1] = {joined(block, at & 15, q)};
+        activate<sizeof(E) == 4>(y, a.act);
+        a.H[(int64_t)L.list[L.first[slot(p)] + at] * a.f + c] = to_elem<E>(y[0] * joined(block, at & 15, 8 + q));
+    }
+};
+
+template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs<E> a) {
+    __shared__ __align__(16) UpLds lds;
+    lds.slots.build(a.ids, a.T * a.k, a.experts, reinterpret_cast<int *>(lds.stream.ring));
+    const UpPositions<E> positions(a, lds.slots);
+    stream_products<E, SLABS, 2>(positions, (int)(a.c * (int)sizeof(E)), lds.stream);
 }
 
 // Y = R + sum_j w_j H_j Wd_e^T.  A workgroup owns ROWS output features of a chunk
@@ -293,12 +245,21 @@ template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe
 // those of a first slot that the run before began: these go to the wavefront's
 // own place and are added afterwards in the order of the wavefronts.  At the end
 // each token's places are added in order.
-template <typename E, int ROWS> __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk) {
-    __shared__ __align__(16) char ring_mem[kWaves * kRingBytes];
-    __shared__ __align__(16) float P[kDownPairs * ROWS];
-    __shared__ __align__(16) float head[kWaves][16 * ROWS];
-    __shared__ Slots<kDownPairs, 16> L;
-    __shared__ float weight[kDownPairs];
+template <int ROWS, int SLOT> struct DownLds {
+    char ring[kWaves * kRingBytes];
+    float sums[kDownPairs<ROWS> * ROWS];  // of every pair
+    float head[kWaves][16 * ROWS];        // of a run's first slot, begun by the run before
+    float weight[kDownPairs<ROWS>];
+    Slots<kDownPairs<ROWS>, SLOT> slots;
+};
+// Slots hold SLOT pairs: of 8, the ring holds more weights; of 16, an expert of
+// more than 8 pairs is read once.
+template <typename E, int ROWS, int SLOT>
+__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk) {
+    __shared__ __align__(16) DownLds<ROWS, SLOT> lds;
+    float *const P = lds.sums, *const weight = lds.weight;
+    auto &L = lds.slots;
+    auto &head = lds.head;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i16 = lane & 15, g = lane >> 4;
@@ -314,8 +275,7 @@ template <typename E, int ROWS> __global__ __launch_bounds__(kThreads) void moe_
             for (int q = 0; q < ROWS; ++q) P[p * ROWS + q] = 0.f;
         }
     }
-    L.build(ids, places, a.experts, reinterpret_cast<int *>(ring_mem),
-            reinterpret_cast<int *>(ring_mem) + kMoeMaxExperts);
+    L.build(ids, places, a.experts, reinterpret_cast<int *>(lds.ring));
     const int row_bytes = (int)(a.f * (int)sizeof(E));
     const int slabs = (row_bytes + 127) / 128;
     const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * slabs;
@@ -323,7 +283,7 @@ template <typename E, int ROWS> __global__ __launch_bounds__(kThreads) void moe_
     const int64_t r0 = run_start(wave), r1 = run_start(wave + 1);
 
     SlabRows w, x;
-    SlabRing<E, true, ROWS> ring{ring_mem + wave * kRingBytes};
+    SlabRing<E, ROWS, SLOT> ring{lds.ring + wave * kRingBytes};
     int64_t in_left = r1 - r0;
     int in_slot = (int)(r0 / slabs), in_slab = (int)(r0 % slabs);
     x.buf[0] = x.buf[1] = panel(a.H + (int64_t)t0 * a.k * a.f);
@@ -400,9 +360,9 @@ template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipSt
     hipLaunchKernelGGL((moe_up_kernel<E, SLABS>), dim3((unsigned)std::min<int64_t>(most, 256)), dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
-template <typename E, int ROWS> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
-    const int chunk = std::min(a.T, kDownPairs / a.k);
-    hipLaunchKernelGGL((moe_down_kernel<E, ROWS>),
+template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
+    const int chunk = std::min(a.T, kDownPairs<ROWS> / a.k);
+    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>),
                        dim3((unsigned)((a.c + ROWS - 1) / ROWS), (unsigned)((a.T + chunk - 1) / chunk)), dim3(kThreads),
                        0, st, a, chunk);
     return hipGetLastError();
@@ -438,8 +398,12 @@ template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st)
                          : slabs <= 8 ? launch_up<E, 8>(a, st)
                                       : launch_up<E, 12>(a, st);
     if (e != hipSuccess) return e;
-    // 8 rows a workgroup where 16 would leave CUs without one
-    return a.c <= 16 * 255 ? launch_down<E, 8>(a, st) : launch_down<E, 16>(a, st);
+    // 8 rows a workgroup where 16 would leave CUs without one or read the
+    // weights for a second chunk of tokens; slots of 8 where experts have 4 pairs
+    // on average
+    const bool few = a.T <= 8 || pairs <= 6 * a.experts;
+    if (a.c <= 16 * 255 || pairs > kDownPairs<16>) return few ? launch_down<E, 8, 8>(a, st) : launch_down<E, 8, 16>(a, st);
+    return few ? launch_down<E, 16, 8>(a, st) : launch_down<E, 16, 16>(a, st);
 }
 
 template hipError_t launch_route<float>(const float *, int64_t, int64_t, int, int, bool, bool, float, int32_t *, float *,

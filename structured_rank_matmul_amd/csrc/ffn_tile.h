@@ -27,10 +27,12 @@ __device__ __forceinline__ f32x4 mma32(f32x4 acc, f32x8 a, f32x8 b) {
     return acc;
 }
 
-// A buffer resource over 2 GiB from `p` on; loads at kOutside and beyond give 0.
+// A buffer resource over `bytes` (at most 2 GiB) from `p` on; loads past them, at
+// kOutside among them, give 0.
 constexpr uint32_t kOutside = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t panel(const void *p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)(kOutside - 1), 0x00027000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t panel(const void *p, int64_t bytes = kOutside - 1) {
+    const int n = bytes < (int64_t)kOutside - 1 ? (int)bytes : (int)(kOutside - 1);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00027000);
 }
 __device__ __forceinline__ void buffer_to_lds16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char *lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, (int)voff, (int)soff, 0, 0);

@@ -179,62 +179,70 @@ struct UpLds {
     StreamLds<2> stream;
     Slots<kMoeMaxPairs, kUpSlot> slots;
 };
-template <typename E> struct UpPositions {
+template <typename E> struct UpPosition {
     static constexpr int kFinishers = 8 * kUpSlot;
-    const MoeArgs<E> &a;
-    const Slots<kMoeMaxPairs, kUpSlot> &L;
-    int tiles, u0, count;
-    __device__ UpPositions(const MoeArgs<E> &args, const Slots<kMoeMaxPairs, kUpSlot> &slots) : a(args), L(slots) {
-        tiles = (int)((a.f + 7) / 8);
-        const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * tiles;
-        u0 = (int)(total * blockIdx.x / gridDim.x);
-        count = (int)(total * (blockIdx.x + 1) / gridDim.x) - u0;
+    const MoeArgs<E> *a;
+    const Slots<kMoeMaxPairs, kUpSlot> *L;
+    int tiles, left, slot, tile, pairs;
+    int64_t row;  // of this tile in the stacked [experts * f] rows
+    __device__ UpPosition(const MoeArgs<E> &args, const Slots<kMoeMaxPairs, kUpSlot> &slots) : a(&args), L(&slots) {
+        tiles = (int)((a->f + 7) / 8);
+        const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L->n) * tiles;
+        const int u0 = (int)(total * blockIdx.x / gridDim.x);
+        left = (int)(total * (blockIdx.x + 1) / gridDim.x) - u0;
+        slot = u0 / tiles;
+        tile = u0 % tiles;
+        enter();
+        row += 8 * (int64_t)tile;
     }
-    __device__ __forceinline__ int slot(int p) const { return (u0 + p) / tiles; }
-    __device__ __forceinline__ int tile(int p) const { return (u0 + p) % tiles; }
-    __device__ __forceinline__ int pairs(int p) const { return __builtin_amdgcn_readfirstlane(L.count[slot(p)]); }
-    __device__ __forceinline__ void weights(int p, SlabRows &w) const {
-        const int e = __builtin_amdgcn_readfirstlane(L.expert[slot(p)]), t = tile(p);
-        const int64_t row = (int64_t)e * a.f + 8 * (int64_t)t;
-        w.buf[0] = panel(a.Wg + row * a.c);
-        w.buf[1] = panel(a.Wu + row * a.c);
-        const int last = (int)min((int64_t)8, a.f - 8 * (int64_t)t) - 1;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            w.off[q] = (uint32_t)min(slab_row(q) & 7, last) * (uint32_t)(a.c * sizeof(E)) + slab_chunk(q);
+    __device__ __forceinline__ void enter() {
+        pairs = __builtin_amdgcn_readfirstlane(L->count[slot]);
+        row = (int64_t)__builtin_amdgcn_readfirstlane(L->expert[slot]) * a->f;
     }
-    __device__ __forceinline__ bool new_tokens(int p) const { return p == 0 || tile(p) == 0; }
-    __device__ __forceinline__ int blocks(int p) const { return pairs(p) > 16 ? 2 : 1; }
-    __device__ __forceinline__ void tokens(int p, SlabRows (&x)[2]) const {
-        const int n = pairs(p), first = L.first[slot(p)];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            x[t].buf[0] = x[t].buf[1] = panel(a.X);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {  // rows past the slot's pairs read nothing
-                const int at = 16 * t + slab_row(q);
-                x[t].off[q] = kOutside;
-                if (at < n)
-                    x[t].off[q] = (uint32_t)(L.list[first + at] / a.k) * (uint32_t)(a.ldx * sizeof(E)) + slab_chunk(q);
-            }
+    __device__ __forceinline__ void advance() {
+        row += 8;
+        if (++tile == tiles) {
+            tile = 0;
+            ++slot;
+            enter();
         }
     }
-    __device__ __forceinline__ void finish(int p, const float *sums, int thread) const {
+    __device__ __forceinline__ void weights(SlabRows &w, bool fresh) const {
+        // rows past f are the next expert's or lie past the end of the buffer:
+        // their products are not stored
+        const int64_t bytes = ((int64_t)a->experts * a->f - row) * a->c * (int64_t)sizeof(E);
+        w.buf[0] = panel(a->Wg + row * a->c, bytes);
+        w.buf[1] = panel(a->Wu + row * a->c, bytes);
+        if (!fresh) return;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            w.off[q] = (uint32_t)(slab_row(q) & 7) * (uint32_t)(a->c * sizeof(E)) + slab_chunk(q);
+    }
+    __device__ __forceinline__ bool new_tokens() const { return tile == 0; }
+    __device__ __forceinline__ int blocks() const { return pairs > 16 ? 2 : 1; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t tokens() const { return panel(a->X); }
+    __device__ __forceinline__ uint32_t token_row(int t) const {
+        const int at = 16 * t + (threadIdx.x & 15);
+        if (at >= pairs) return kOutside;
+        return (uint32_t)(L->list[L->first[slot] + at] / a->k) * (uint32_t)(a->ldx * sizeof(E));
+    }
+    __device__ __forceinline__ void finish(const float *sums, int thread) const {
         const int q = thread & 7, at = thread >> 3;
-        const int64_t c = 8 * (int64_t)tile(p) + q;
-        if (at >= pairs(p) || c >= a.f) return;
+        const int64_t c = 8 * (int64_t)tile + q;
+        if (at >= pairs || c >= a->f) return;
         const float *block = sums + (at >> 4) * kWaves * kBlockSums;
         float y[1] = {joined(block, at & 15, q)};
-        activate<sizeof(E) == 4>(y, a.act);
-        a.H[(int64_t)L.list[L.first[slot(p)] + at] * a.f + c] = to_elem<E>(y[0] * joined(block, at & 15, 8 + q));
+        activate<sizeof(E) == 4>(y, a->act);
+        a->H[(int64_t)L->list[L->first[slot] + at] * a->f + c] = to_elem<E>(y[0] * joined(block, at & 15, 8 + q));
     }
 };
 
 template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs<E> a) {
     __shared__ __align__(16) UpLds lds;
     lds.slots.build(a.ids, a.T * a.k, a.experts, reinterpret_cast<int *>(lds.stream.ring));
-    const UpPositions<E> positions(a, lds.slots);
-    stream_products<E, SLABS, 2>(positions, (int)(a.c * (int)sizeof(E)), lds.stream);
+    if (lds.slots.n == 0) return;
+    const UpPosition<E> start(a, lds.slots);
+    stream_products<E, SLABS, 2>(start, (int)(a.c * (int)sizeof(E)), lds.stream);
 }
 
 // Y = R + sum_j w_j H_j Wd_e^T.  A workgroup owns ROWS output features of a chunk
@@ -299,8 +307,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         }
     };
     auto ahead = [&]() __attribute__((always_inline)) {
-        if (in_left == 0) return;
-        ring.issue(w, x, 128u * (uint32_t)in_slab, row_bytes - 128 * in_slab);
+        ring.issue(w, x, 128u * (uint32_t)in_slab, in_left > 0 ? row_bytes - 128 * in_slab : 0);
         --in_left;
         if (++in_slab == slabs) {
             in_slab = 0;
@@ -309,6 +316,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         }
     };
     if (in_left > 0) aim();
+    else w.buf[0] = w.buf[1] = x.buf[0];  // a run of nothing
 #pragma unroll 1
     for (int p = 0; p < ring.DEPTH; ++p) ahead();
 
@@ -333,6 +341,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
             ++slot;
         }
     }
+    wait_vmcnt<0>();
     __syncthreads();
     if (tid < 16 * ROWS) {  // this thread's column and row of every slot that a run continued
         const int i = tid / ROWS, q = tid % ROWS;

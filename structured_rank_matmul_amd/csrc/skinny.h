@@ -58,16 +58,39 @@ template <typename E, int ROWS> __device__ __forceinline__ SlabFrag<E> slab_read
     }
     return r;
 }
+// The same fragments from global memory: `row` this lane's row's offset in the
+// buffer (kOutside: zeros), `k` the slab's first byte, `left` the bytes of the rows
+// from there on.
+template <typename E> __device__ __forceinline__ SlabFrag<E> slab_load(__amdgpu_buffer_rsrc_t buf, uint32_t row, uint32_t k,
+                                                                      int left) {
+    const uint32_t g = (threadIdx.x & 63) >> 4;
+    SlabFrag<E> r;
+    auto chunk = [&](uint32_t c) -> u32x4 {
+        return __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(16 * c) < left ? row + 16 * c : kOutside, (int)k, 0);
+    };
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) r.f[h] = __builtin_bit_cast(bf16x8, chunk(4 * h + g));
+    } else {
+        const f32x4 lo = __builtin_bit_cast(f32x4, chunk(2 * g)), hi = __builtin_bit_cast(f32x4, chunk(2 * g + 1));
+        r.f[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return r;
+}
+
 constexpr int kRingBytes = 16384;  // of LDS for each wavefront's ring
 
-// One wavefront's ring of slabs: WROWS rows of weights and XROWS of tokens (16
-// or 8 each, XROWS also 0; with 8, rows 8 .. 15 of the fragments repeat them).
+// One wavefront's ring of slabs, always full: DEPTH slabs are issued at first and
+// one more after each is taken, past the end of the stream slabs of nothing (no
+// byte left: zeros, no memory is read), so that one wait fits every take.  The
+// copies left over have to land before the workgroup ends.  WROWS rows of
+// weights and XROWS of tokens a slab (16 or 8 each, XROWS also 0; with 8, rows
+// 8 .. 15 of the fragments repeat them).
 template <typename E, int WROWS, int XROWS> struct SlabRing {
     static constexpr int WBYTES = 128 * WROWS, SLAB = WBYTES + 128 * XROWS;
     static constexpr int DEPTH = kRingBytes / SLAB, COPIES = (WROWS + XROWS) / 8;
     char *ring;            // this wavefront's kRingBytes of LDS
-    int ahead = 0;             // slabs issued and not consumed
-    int put = 0, got = 0;      // places of the next slab to issue and to consume
+    int at = 0;            // place of the oldest slab, and of the next to issue
 
     template <int ROWS> __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
 #pragma unroll
@@ -77,45 +100,45 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
     // Copies one slab at byte `k` of the rows; `left` bytes of the rows are left.
     __device__ __forceinline__ void issue(const SlabRows &w, uint32_t k, int left) { issue(w, w, k, left); }
     __device__ __forceinline__ void issue(const SlabRows &w, const SlabRows &x, uint32_t k, int left) {
-        char *dst = ring + put * SLAB;
+        char *dst = ring + at * SLAB;
         copy<WROWS>(w, k, left, dst);
         if constexpr (XROWS > 0) copy<XROWS>(x, k, left, dst + WBYTES);
-        put = put + 1 == DEPTH ? 0 : put + 1;
-        ++ahead;
+        at = at + 1 == DEPTH ? 0 : at + 1;
     }
-    // Waits for the oldest slab and reads its fragments; its place is then free.
+    // Waits for the oldest slab and reads its fragments; the next issue has to
+    // follow, into its place.
     __device__ __forceinline__ void take(SlabFrag<E> &w) {
         SlabFrag<E> none;
         take(w, none);
     }
     __device__ __forceinline__ void take(SlabFrag<E> &w, SlabFrag<E> &x) {
         // (stores issued in between only make the wait stricter)
-        if (ahead == DEPTH) wait_vmcnt<(DEPTH - 1) * COPIES>();
-        else wait_vmcnt<0>();
+        wait_vmcnt<(DEPTH - 1) * COPIES>();
         // the copies write LDS behind the compiler's back: no read may move above the wait
         asm volatile("" ::: "memory");
-        const char *slab = ring + got * SLAB;
+        const char *slab = ring + at * SLAB;
         w = slab_read<E, WROWS>(slab);
         if constexpr (XROWS > 0) x = slab_read<E, XROWS>(slab + WBYTES);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the fragments are in registers
         asm volatile("" ::: "memory");
-        got = got + 1 == DEPTH ? 0 : got + 1;
-        --ahead;
     }
 };
 
-// The products of a sequence of positions: position p multiplies 16 weight rows
+// The products of a sequence of positions: a position multiplies 16 weight rows
 // with one or two blocks of 16 tokens.  The workgroup's eight wavefronts split K,
 // each running its part of every position through one ring without a break.  The
-// tokens' fragments come through the same ring, ahead of the weights that they
-// meet, and stay in registers (SLABS slabs of K, TB blocks) until a position with
-// other tokens; where a wavefront has more than SLABS slabs they pass anew for
-// every position.  The wavefronts' sums meet in LDS, added in their order.
+// tokens' fragments stay in registers (SLABS slabs of K, TB blocks) until a
+// position with other tokens; where a wavefront has more than SLABS slabs they are
+// loaded anew for every position, and the ring drains each time.  The wavefronts'
+// sums meet in LDS, added in their order.
 //
-// A Positions type gives: count; weights(p, SlabRows &); new_tokens(p), whether
-// p's differ from p - 1's; tokens(p, SlabRows (&)[TB]); blocks(p), 1 .. TB;
-// finish(p, sums, thread), called by all threads with sums of 16 tokens x 16
-// rows per block and wavefront.  All but finish must give wave-uniform answers.
+// A Position type stands at one of the sequence and gives: left, the positions
+// from it on; advance(); weights(SlabRows &), with `fresh` set the rows' offsets
+// too (they are the same at every position); new_tokens(), whether its tokens
+// differ from those of the position before; blocks(), 1 .. TB; tokens(), their
+// buffer; token_row(t), this lane's row (lane % 16) of block t in it; finish(sums,
+// thread), called by all threads with sums of 16 tokens x 16 rows per block and
+// wavefront.  All but token_row and finish give wave-uniform answers.
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kBlockSums = 256;  // floats of a block's sums: token, then row
@@ -133,8 +156,8 @@ template <int TB> struct StreamLds {
     float sums[2][kWaves][kBlockSums];
 };
 
-template <typename E, int SLABS, int TB, class Positions>
-__device__ __forceinline__ void stream_products(const Positions &P, int row_bytes, StreamLds<TB> &lds) {
+template <typename E, int SLABS, int TB, class Position>
+__device__ __forceinline__ void stream_products(const Position &start, int row_bytes, StreamLds<TB> &lds) {
     static_assert(TB == 1 || TB == 2, "token blocks");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -142,59 +165,59 @@ __device__ __forceinline__ void stream_products(const Positions &P, int row_byte
     const int s0 = min(slabs, wave * per), s1 = min(slabs, s0 + per);  // this wavefront's slabs
     const bool parts = s1 - s0 > SLABS;  // the tokens do not stay
 
-    // the stream: position, slabs from `in_base` on; tokens first where they are due
-    SlabRing<E, 16, 0> ring{lds.ring + wave * kRingBytes};
-    SlabRows w, x[TB];
-    int in_pos = s0 == s1 ? P.count : 0, in_base = s0, in_slab = 0, in_block = 0, in_blocks = 0;
-    auto aim = [&]() __attribute__((always_inline)) {
-        P.weights(in_pos, w);
-        if (parts || P.new_tokens(in_pos)) {
-            P.tokens(in_pos, x);
-            in_blocks = P.blocks(in_pos);
+    SlabFrag<E> fx[TB][SLABS];
+    auto load_tokens = [&](const Position &at, int base) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t buf = at.tokens();
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const uint32_t row = at.token_row(t);
+            if (t > 0 && at.blocks() == 1) continue;
+#pragma unroll
+            for (int j = 0; j < SLABS; ++j)  // slabs past s1 are not used
+                fx[t][j] = slab_load<E>(buf, row, 128u * (uint32_t)(base + j), row != kOutside ? row_bytes - 128 * (base + j) : 0);
         }
     };
+    // loads return in order: with the tokens first, the first slab is multiplied
+    // as soon as it lands
+    load_tokens(start, s0);
+    asm volatile("" ::: "memory");
+
+    // the stream of weights: slabs s0 .. s1 of position after position
+    SlabRing<E, 16, 0> ring{lds.ring + wave * kRingBytes};
+    SlabRows w;
+    Position in = start;
+    int in_slab = s0;
+    if (s0 == s1) in.left = 0;
+    in.weights(w, true);
     auto ahead = [&]() __attribute__((always_inline)) {
-        if (in_pos == P.count) return;
-        const int n = min(SLABS, s1 - in_base), s = in_base + in_slab;
-        const uint32_t k = 128u * (uint32_t)s;
-        const int left = row_bytes - 128 * s;
-        const bool last = ++in_slab == n;
-        if (last) in_slab = 0;
-        if (in_block < in_blocks) {
-            ring.issue(TB == 2 && in_block == 1 ? x[TB - 1] : x[0], k, left);
-            if (last) ++in_block;
-        } else {
-            ring.issue(w, k, left);
-            if (last) {
-                in_block = 0;
-                in_base += SLABS;
-                if (in_base >= s1) {
-                    in_base = s0;
-                    in_blocks = 0;
-                    if (++in_pos < P.count) aim();
-                }
+        ring.issue(w, 128u * (uint32_t)in_slab, in.left > 0 ? row_bytes - 128 * in_slab : 0);
+        if (++in_slab >= s1) {
+            in_slab = s0;
+            if (--in.left > 0) {
+                in.advance();
+                in.weights(w, false);
             }
         }
     };
-    if (in_pos < P.count) aim();
-#pragma unroll 1
+#pragma unroll
     for (int q = 0; q < ring.DEPTH; ++q) ahead();
+    // said to the compiler as well: the tokens are in their registers, and no wait
+    // for them stands between the products
+    wait_vmcnt<ring.DEPTH * ring.COPIES>();
 
-    SlabFrag<E> fx[TB][SLABS];
     int set = 1, begin = 0;
-    bool was_two = false;
-    for (int p = 0; p < P.count; ++p) {
-        const bool two = TB == 2 && P.blocks(p) == 2;
+    bool was_two = false, stale = parts;
+    for (Position at = start; at.left > 0; --at.left) {
+        if (at.left != start.left) {
+            at.advance();
+            stale = parts || at.new_tokens();
+        }
+        const bool two = TB == 2 && at.blocks() == 2;
         f32x4 acc[TB] = {};
         for (int base = s0; base < s1; base += SLABS) {
-            if (parts || P.new_tokens(p)) {
-#pragma unroll
-                for (int t = 0; t < TB; ++t)
-                    if (t == 0 || two) unroll_seq<SLABS>([&](auto j) __attribute__((always_inline)) {
-                        if (base + (int)j >= s1) return;
-                        ring.take(fx[t][j]);
-                        ahead();
-                    });
+            if (stale) {
+                load_tokens(at, base);
+                wait_vmcnt<0>();
             }
             unroll_seq<SLABS>([&](auto j) __attribute__((always_inline)) {
                 if (base + (int)j >= s1) return;
@@ -215,9 +238,10 @@ __device__ __forceinline__ void stream_products(const Positions &P, int row_byte
         *reinterpret_cast<f32x4 *>(mine) = acc[0];
         if (two) *reinterpret_cast<f32x4 *>(mine + kWaves * kBlockSums) = acc[TB - 1];
         __syncthreads();
-        P.finish(p, &lds.sums[set][0][0], (tid - begin) & (kThreads - 1));
-        begin += Positions::kFinishers;  // other wavefronts finish the next one
+        at.finish(&lds.sums[set][0][0], (tid - begin) & (kThreads - 1));
+        begin += Position::kFinishers;  // other wavefronts finish the next one
     }
+    wait_vmcnt<0>();
 }
 
 }  // namespace dyra

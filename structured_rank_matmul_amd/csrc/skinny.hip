@@ -2,11 +2,10 @@
 //
 // A workgroup takes units of 16 weight rows (16 output features, or 8 gate and
 // the same 8 up rows) and streams them through its wavefronts' rings (skinny.h);
-// a unit's epilogue runs while the next unit's slabs are landing.  More than 16
-// TB tokens are taken in groups, one after the other on the same unit.
-//
-// 16 tokens, gated 4096 -> 14336 (235 MB of weights): see kSkinnyTokens in
-// ffn_api.hip for what the other kernel takes.
+// a unit's epilogue runs while the next unit's slabs are landing.  Tokens that
+// fit stay in registers (skinny_kernel); others go through the ring beside the
+// weights, in groups of 16 on the same unit (skinny_ring_kernel): 16 tokens, gated
+// 4096 -> 14336 (235 MB of weights), 43 us against 54.
 #include "skinny.h"
 
 #include <algorithm>
@@ -15,69 +14,132 @@ namespace dyra {
 
 namespace {
 
-template <typename E, typename O, bool GATED, int TB> struct UnitPositions {
-    static constexpr int R = GATED ? 8 : 16;            // output features of a unit
-    static constexpr int kFinishers = 16 * R * TB;
-    const LinearArgs<E, O> &a;
-    int units, groups, count;
-    __device__ UnitPositions(const LinearArgs<E, O> &args, int n, int g) : a(args), units(n), groups(g) {
-        count = (n - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * g;
-    }
-    __device__ __forceinline__ int unit(int p) const { return (int)blockIdx.x + p / groups * (int)gridDim.x; }
-    __device__ __forceinline__ int64_t token0(int p) const { return 16 * TB * (int64_t)(p % groups); }
-    __device__ __forceinline__ void weights(int p, SlabRows &w) const {
-        const int64_t f0 = (int64_t)unit(p) * R;
-        const uint32_t ld = (uint32_t)(a.ldw * sizeof(E));
-        const int last = (int)min((int64_t)R, a.N - f0) - 1;  // rows past the end repeat the last one
-        w.buf[0] = panel(a.W0 + f0 * a.ldw);
-        w.buf[1] = GATED ? panel(a.W1 + f0 * a.ldw) : w.buf[0];
+// Units of 16 weight rows: where they lie, and what becomes of their sums.
+template <typename E, typename O, bool GATED> struct Units {
+    static constexpr int R = GATED ? 8 : 16;  // output features
+    const LinearArgs<E, O> *a;
+    __device__ __forceinline__ void weights(int unit, SlabRows &w, bool fresh) const {
+        // rows past the last one lie past the end of the buffer
+        const int64_t from = (int64_t)unit * R * a->ldw;
+        const int64_t bytes = ((a->N - 1) * a->ldw + a->K - from) * (int64_t)sizeof(E);
+        w.buf[0] = panel(a->W0 + from, bytes);
+        w.buf[1] = GATED ? panel(a->W1 + from, bytes) : w.buf[0];
+        if (!fresh) return;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            w.off[q] = (uint32_t)min(GATED ? slab_row(q) & 7 : slab_row(q), last) * ld + slab_chunk(q);
+            w.off[q] = (uint32_t)(GATED ? slab_row(q) & 7 : slab_row(q)) * (uint32_t)(a->ldw * sizeof(E)) + slab_chunk(q);
     }
-    __device__ __forceinline__ bool new_tokens(int p) const { return p == 0 || groups > 1; }
-    __device__ __forceinline__ int blocks(int p) const { return TB == 2 && a.M - token0(p) > 16 ? 2 : 1; }
-    __device__ __forceinline__ void tokens(int p, SlabRows (&x)[TB]) const {
-        const int64_t t0 = token0(p);
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            x[t].buf[0] = x[t].buf[1] = panel(a.X + t0 * a.ldx);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {  // rows past the end read nothing
-                const int r = 16 * t + slab_row(q);
-                x[t].off[q] = t0 + r < a.M ? (uint32_t)r * (uint32_t)(a.ldx * sizeof(E)) + slab_chunk(q) : kOutside;
-            }
-        }
-    }
-    __device__ __forceinline__ void finish(int p, const float *sums, int thread) const {
+    // Token t and feature f of the unit, from token `first` on.
+    __device__ __forceinline__ void finish(int unit, int64_t first, const float *sums, int thread, int tokens) const {
         const int f = thread % R, t = thread / R;
-        const int64_t tok = token0(p) + t, c = (int64_t)unit(p) * R + f;
-        if (t >= 16 * TB || tok >= a.M || c >= a.N) return;
+        const int64_t tok = first + t, c = (int64_t)unit * R + f;
+        if (t >= tokens || tok >= a->M || c >= a->N) return;
         const float *block = sums + (t >> 4) * kWaves * kBlockSums;
-        float y[1] = {joined(block, t & 15, f) + (a.b0 ? to_f32(a.b0[c]) : 0.f)};
-        activate<sizeof(O) == 4>(y, a.act);
-        if constexpr (GATED) y[0] *= joined(block, t & 15, 8 + f) + (a.b1 ? to_f32(a.b1[c]) : 0.f);
-        else if (a.R) y[0] += to_f32(a.R[tok * a.ldr + c]);
-        a.Y[tok * a.ldy + c] = to_elem<O>(y[0]);
+        float y[1] = {joined(block, t & 15, f) + (a->b0 ? to_f32(a->b0[c]) : 0.f)};
+        activate<sizeof(O) == 4>(y, a->act);
+        if constexpr (GATED) y[0] *= joined(block, t & 15, 8 + f) + (a->b1 ? to_f32(a->b1[c]) : 0.f);
+        else if (a->R) y[0] += to_f32(a->R[tok * a->ldr + c]);
+        a->Y[tok * a->ldy + c] = to_elem<O>(y[0]);
+    }
+};
+
+template <typename E, typename O, bool GATED, int TB> struct UnitPosition {
+    static constexpr int kFinishers = 16 * TB * Units<E, O, GATED>::R;
+    Units<E, O, GATED> units;
+    int left, unit;
+    __device__ UnitPosition(const LinearArgs<E, O> &a, int n) : units{&a}, unit((int)blockIdx.x) {
+        left = (n - unit + (int)gridDim.x - 1) / (int)gridDim.x;
+    }
+    __device__ __forceinline__ void advance() { unit += (int)gridDim.x; }
+    __device__ __forceinline__ void weights(SlabRows &w, bool fresh) const { units.weights(unit, w, fresh); }
+    __device__ __forceinline__ bool new_tokens() const { return false; }
+    __device__ __forceinline__ int blocks() const { return TB; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t tokens() const { return panel(units.a->X); }
+    __device__ __forceinline__ uint32_t token_row(int t) const {
+        const int r = 16 * t + (threadIdx.x & 15);
+        return r < units.a->M ? (uint32_t)r * (uint32_t)(units.a->ldx * sizeof(E)) : kOutside;
+    }
+    __device__ __forceinline__ void finish(const float *sums, int thread) const {
+        units.finish(unit, 0, sums, thread, 16 * TB);
     }
 };
 
 template <typename E, typename O, bool GATED, int SLABS, int TB>
-__global__ __launch_bounds__(kThreads) void skinny_kernel(LinearArgs<E, O> a, int units, int groups) {
+__global__ __launch_bounds__(kThreads) void skinny_kernel(LinearArgs<E, O> a, int units) {
     __shared__ __align__(16) StreamLds<TB> lds;
-    const UnitPositions<E, O, GATED, TB> positions(a, units, groups);
-    stream_products<E, SLABS, TB>(positions, (int)(a.K * (int)sizeof(E)), lds);
+    const UnitPosition<E, O, GATED, TB> start(a, units);
+    stream_products<E, SLABS, TB>(start, (int)(a.K * (int)sizeof(E)), lds);
+}
+
+template <typename E, typename O, bool GATED>
+__global__ __launch_bounds__(kThreads) void skinny_ring_kernel(LinearArgs<E, O> a, int units, int groups) {
+    __shared__ __align__(16) StreamLds<1> lds;
+    const Units<E, O, GATED> U{&a};
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row_bytes = (int)(a.K * (int)sizeof(E));
+    const int slabs = (row_bytes + 127) / 128, per = (slabs + kWaves - 1) / kWaves;
+    const int s0 = min(slabs, wave * per), s1 = min(slabs, s0 + per);  // this wavefront's slabs
+
+    // the stream: slabs s0 .. s1 of segment after segment (unit, token group)
+    SlabRing<E, 16, 16> ring{lds.ring + wave * kRingBytes};
+    SlabRows w, x;
+    const uint32_t xld = (uint32_t)(a.ldx * sizeof(E));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) x.off[q] = (uint32_t)slab_row(q) * xld + slab_chunk(q);
+    int in_unit = s0 < s1 ? (int)blockIdx.x : units, in_group = 0, in_slab = s0;
+    auto aim_tokens = [&]() __attribute__((always_inline)) {
+        const int64_t from = 16 * (int64_t)in_group * a.ldx;
+        x.buf[0] = x.buf[1] = panel(a.X + from, ((a.M - 1) * a.ldx + a.K - from) * (int64_t)sizeof(E));
+    };
+    U.weights(min(in_unit, units - 1), w, true);
+    aim_tokens();
+    auto ahead = [&]() __attribute__((always_inline)) {
+        ring.issue(w, x, 128u * (uint32_t)in_slab, in_unit < units ? row_bytes - 128 * in_slab : 0);
+        if (++in_slab >= s1) {
+            in_slab = s0;
+            if (++in_group == groups) {
+                in_group = 0;
+                in_unit += (int)gridDim.x;
+                if (in_unit < units) U.weights(in_unit, w, false);
+            }
+            if (groups > 1) aim_tokens();
+        }
+    };
+#pragma unroll 1
+    for (int q = 0; q < ring.DEPTH; ++q) ahead();
+
+    int set = 0, begin = 0;
+    for (int u = blockIdx.x; u < units; u += (int)gridDim.x) {
+        for (int group = 0; group < groups; ++group, set ^= 1) {
+            f32x4 acc = {};
+#pragma unroll 1
+            for (int s = s0; s < s1; ++s) {
+                SlabFrag<E> fw, fx;
+                ring.take(fw, fx);
+                ahead();
+                acc = slab_product(acc, fw, fx);
+            }
+            // two sets of sums: one is read while the next segment's is written
+            *reinterpret_cast<f32x4 *>(&lds.sums[set][wave][(lane & 15) * 16 + 4 * (lane >> 4)]) = acc;
+            __syncthreads();
+            U.finish(u, 16 * (int64_t)group, &lds.sums[set][0][0], (tid - begin) & (kThreads - 1), 16);
+            begin += 16 * U.R;  // other wavefronts finish the next one
+        }
+    }
+    wait_vmcnt<0>();
+}
+
+// At most one workgroup per CU, the same number of units each (224 x 4 units
+// rather than 128 x 4 and 128 x 3: 16 tokens, 4096 -> 14336, 29.4 -> 24.4 us).
+inline unsigned workgroups(int units) {
+    const int rounds = (units + 255) / 256;
+    return (unsigned)((units + rounds - 1) / rounds);
 }
 
 template <typename E, typename O, bool GATED, int SLABS, int TB>
-hipError_t launch_slabs(const LinearArgs<E, O> &a, hipStream_t st) {
-    const int units = (int)((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
-    const int groups = (int)((a.M + 16 * TB - 1) / (16 * TB));
-    // at most one workgroup per CU, the same number of units each (224 x 4 units
-    // rather than 128 x 4 and 128 x 3: 16 tokens, 4096 -> 14336, 29.4 -> 24.4 us)
-    const int rounds = (units + 255) / 256;
-    hipLaunchKernelGGL((skinny_kernel<E, O, GATED, SLABS, TB>), dim3((unsigned)((units + rounds - 1) / rounds)),
-                       dim3(kThreads), 0, st, a, units, groups);
+hipError_t launch_slabs(const LinearArgs<E, O> &a, int units, hipStream_t st) {
+    hipLaunchKernelGGL((skinny_kernel<E, O, GATED, SLABS, TB>), dim3(workgroups(units)), dim3(kThreads), 0, st, a, units);
     return hipGetLastError();
 }
 
@@ -85,19 +147,25 @@ hipError_t launch_slabs(const LinearArgs<E, O> &a, hipStream_t st) {
 
 template <typename E, typename O, bool GATED> hipError_t launch_skinny(const LinearArgs<E, O> &a, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    // the smallest register space that holds a wavefront's slabs of the tokens
-    // (8 registers a slab and block), or the largest that fits
+    const int units = (int)((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
+    // registers hold a wavefront's slabs of the tokens (8 a slab and block of 16)
+    // up to 24 slabs of one block or 12 of two
     const int slabs = (int)((a.K * (int64_t)sizeof(E) + 128 * kWaves - 1) / (128 * kWaves));
-    if (a.M <= 16) {
-        if (slabs <= 2) return launch_slabs<E, O, GATED, 2, 1>(a, st);
-        if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 1>(a, st);
-        if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 1>(a, st);
-        if (slabs <= 16) return launch_slabs<E, O, GATED, 16, 1>(a, st);
-        return launch_slabs<E, O, GATED, 24, 1>(a, st);
+    if (a.M <= 16 && slabs <= 24) {
+        if (slabs <= 2) return launch_slabs<E, O, GATED, 2, 1>(a, units, st);
+        if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 1>(a, units, st);
+        if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 1>(a, units, st);
+        if (slabs <= 16) return launch_slabs<E, O, GATED, 16, 1>(a, units, st);
+        return launch_slabs<E, O, GATED, 24, 1>(a, units, st);
     }
-    if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 2>(a, st);
-    if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 2>(a, st);
-    return launch_slabs<E, O, GATED, 12, 2>(a, st);
+    if (a.M > 16 && a.M <= 32 && slabs <= 12) {
+        if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 2>(a, units, st);
+        if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 2>(a, units, st);
+        return launch_slabs<E, O, GATED, 12, 2>(a, units, st);
+    }
+    hipLaunchKernelGGL((skinny_ring_kernel<E, O, GATED>), dim3(workgroups(units)), dim3(kThreads), 0, st, a, units,
+                       (int)((a.M + 15) / 16));
+    return hipGetLastError();
 }
 
 template hipError_t launch_skinny<bf16, bf16, false>(const LinearArgs<bf16, bf16> &, hipStream_t);

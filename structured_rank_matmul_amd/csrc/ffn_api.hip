@@ -19,7 +19,7 @@ constexpr int64_t kMaxRow = int64_t{1} << 20;
 // addressed from the first.
 constexpr int64_t kMaxExpertRow = int64_t{1} << 18;
 // Up to this many tokens the weights are streamed by skinny_kernel.
-constexpr int64_t kSkinnyTokens = 64;
+constexpr int64_t kSkinnyTokens = 32;
 
 dyra_status hip_status(hipError_t e) { return e == hipSuccess ? DYRA_OK : DYRA_ERR_HIP; }
 bool aligned(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
@@ -60,9 +60,8 @@ template <typename E, typename O, bool GATED>
 dyra_status run_linear(const void *X, int64_t ldx, const void *W0, const void *W1, int64_t ldw, int64_t N, int64_t c1,
                        int64_t c2, const void *b0, const void *b1, dyra_act act, const void *R, int64_t ldr, void *Y,
                        int64_t ldy, void *stream) {
-    const bool vec = aligned(Y, 16) && ldy * sizeof(O) % 16 == 0 && aligned(R, 16) && ldr * sizeof(O) % 16 == 0;
-    const dyra::LinearArgs<E, O> a{(const E *)X,  ldx, (const E *)W0, (const E *)W1, ldw, N,   c1 ? c2 : 0, c1,
-                                   (const E *)b0, (const E *)b1, (const O *)R,   ldr, (O *)Y, ldy, (int)act,    vec};
+    const dyra::LinearArgs<E, O> a{(const E *)X,  ldx, (const E *)W0, (const E *)W1, ldw, N, c2, c1,
+                                   (const E *)b0, (const E *)b1, (const O *)R,   ldr, (O *)Y, ldy, (int)act};
     return run<E, O, GATED>(a, (hipStream_t)stream);
 }
 

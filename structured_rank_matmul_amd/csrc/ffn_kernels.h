@@ -28,7 +28,6 @@ template <typename E, typename O> struct LinearArgs {
     O *Y;              // [M][N], rows ldy apart
     int64_t ldy;
     int act;
-    bool vec;          // rows of Y and R start on 16-byte boundaries
 };
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st);

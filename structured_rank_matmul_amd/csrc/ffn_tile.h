@@ -90,16 +90,18 @@ template <bool PRECISE, int C> __device__ __forceinline__ void activate(float (&
     }
 }
 
-// N consecutive elements as float32 (16-byte accesses where `vec`; only the
-// first `have` exist).
-template <typename T, int N> __device__ __forceinline__ void load_row(const T *p, float (&v)[N], bool vec, int have) {
+// N consecutive elements as float32, of which the first `have` exist: 16-byte
+// accesses of any alignment where all do (gfx950 takes them; rows of odd length
+// stored by elements cost an epilogue of 1501 x 1003 floats 6 us of 14).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <typename T, int N> __device__ __forceinline__ void load_row(const T *p, float (&v)[N], int have) {
     constexpr int V = 16 / (int)sizeof(T);
     static_assert(N % V == 0, "whole 16-byte chunks");
-    if (vec && have >= N) {
+    if (have >= N) {
 #pragma unroll
         for (int q = 0; q < N; q += V) {
             union { u32x4 u; T e[V]; } w;
-            w.u = *reinterpret_cast<const u32x4 *>(p + q);
+            w.u = *reinterpret_cast<const u32x4_any *>(p + q);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[q + i] = to_f32(w.e[i]);
         }
@@ -108,15 +110,15 @@ template <typename T, int N> __device__ __forceinline__ void load_row(const T *p
         for (int q = 0; q < N; ++q) v[q] = q < have ? to_f32(p[q]) : 0.f;
     }
 }
-template <typename T, int N> __device__ __forceinline__ void store_row(T *p, const float (&v)[N], bool vec, int have) {
+template <typename T, int N> __device__ __forceinline__ void store_row(T *p, const float (&v)[N], int have) {
     constexpr int V = 16 / (int)sizeof(T);
-    if (vec && have >= N) {
+    if (have >= N) {
 #pragma unroll
         for (int q = 0; q < N; q += V) {
             union { u32x4 u; T e[V]; } w;
 #pragma unroll
             for (int i = 0; i < V; ++i) w.e[i] = to_elem<T>(v[q + i]);
-            *reinterpret_cast<u32x4 *>(p + q) = w.u;
+            *reinterpret_cast<u32x4_any *>(p + q) = w.u;
         }
     } else {
 #pragma unroll

@@ -1,16 +1,19 @@
-// Linear layer and gated pair for many tokens:
+// Linear layer and gated pair for more tokens than skinny.hip takes:
 //     Y = act(X W^T + b) + R           H = act(X Wg^T + bg) * (X Wu^T + bu)
 // one pass over X and the weights, the epilogue applied to the accumulators.
+// Products that fill the chip with 256 x 256 tiles take linear_big.h's kernel;
+// the tiles here, from 32 x 64 to 128 x 256, are for those that would not.
 //
 // A workgroup owns BM tokens x BF output features (gated: BF features of both
 // products, so a lane holds a feature's gate and up sums together and the
-// pair never reaches memory).  K advances in slices of 128 bytes per row, moved
-// from global memory straight into LDS, NS slices in flight, one barrier per
-// slice.  A slice row is 8 chunks of 16 bytes, chunk c at position c ^ sw(row),
-// so that the 16 rows a 16-lane group reads fall on distinct banks; the swizzle
-// is applied by choosing which chunk each lane of the copy fetches.
-// A last slice that reaches past K fetches the missing chunks from a zero
-// chunk, for both operands.
+// pair never reaches memory).  K advances in stages of SL slabs of 128 bytes per
+// row, copied from global memory straight into LDS, NS stages in flight (100 to
+// 144 KB: with one tile per CU, depth is what hides the latency), one barrier per
+// stage.  A slab row is 8 chunks of 16 bytes, chunk c at position c ^ sw(row), so
+// that the 16 rows a 16-lane group reads fall on distinct banks; the swizzle is
+// applied by choosing which chunk each lane of the copy fetches.  Rows past the
+// end, chunks past K and stages past the last are read out of the buffers'
+// range: zeros, and one wait fits every stage.
 //
 // Output layout: the weights are the first MFMA operand, so a lane's registers
 // run along output features.  Rows of the weight panel are dealt to pairs of
@@ -27,70 +30,69 @@ namespace dyra {
 
 namespace {
 
-__device__ __align__(16) const unsigned g_zero[4] = {0, 0, 0, 0};
-
-template <typename E, int BM, int BF, int WM, int WN, int NS, bool GATED> struct TileShape {
+template <typename E, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED> struct TileShape {
     static constexpr int NW = WM * WN;
     static constexpr int BN = GATED ? 2 * BF : BF;   // rows of the weight panel
     static constexpr int TM = BM / WM / 16;          // token blocks of a wavefront
     static constexpr int TF = BF / WN / 16;          // feature blocks of a wavefront (per product)
     static constexpr int TN = GATED ? 2 * TF : TF;
-    static constexpr int BK = 128 / (int)sizeof(E);  // elements of a slice row
-    static constexpr int BLOCKS = (BM + BN) / 8;     // 1 KB copies per slice
-    static constexpr int PER_WAVE = BLOCKS / NW;
-    static constexpr int STAGE = (BM + BN) * 128;
-    static_assert(BLOCKS % NW == 0 && TF % 2 == 0 && TM >= 1 && BF % 32 == 0, "tile shape");
+    static constexpr int PER_WAVE = (BM + BN) / 8 / NW;  // 1 KB copies of a slab
+    static constexpr int SLAB = (BM + BN) * 128, STAGE = SL * SLAB;
+    static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0 && BF / 8 % NW == 0, "whole copies per panel");
+    static_assert(TF % 2 == 0 && TM >= 1 && BF % 32 == 0 && NS * STAGE <= 160 * 1024, "tile shape");
 };
 
-template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, bool GATED>
+template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles,
                                                                    int per_xcd) {
-    using S = TileShape<E, BM, BF, WM, WN, NS, GATED>;
-    constexpr int VEC = 16 / (int)sizeof(E);
+    using S = TileShape<E, BM, BF, WM, WN, NS, SL, GATED>;
     __shared__ __align__(16) char smem[NS * S::STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int i16 = lane & 15, g = lane >> 4;
     // workgroup ids are dealt round-robin over the 8 XCDs; each XCD walks a
-    // contiguous band of tiles, so tiles that share operands share an L2
+    // contiguous band of tiles, down the tokens first, so tiles that share
+    // weights share an L2
     const int tile = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
     if (tile >= ntiles) return;
-    const int64_t row0 = (int64_t)(tile / tiles_n) * BM;
-    const int64_t col0 = (int64_t)(tile % tiles_n) * BF;
+    const int tiles_m = ntiles / tiles_n;
+    const int64_t row0 = (int64_t)(tile % tiles_m) * BM;
+    const int64_t col0 = (int64_t)(tile / tiles_m) * BF;
 
-    // this wavefront's copies: panel row and chunk per lane (rows past the end
-    // are fetched from the last row and never stored)
-    const char *src[S::PER_WAVE];
-    int chunk[S::PER_WAVE];
+    // this wavefront's copies of a slab: block q of 8 rows, BM / 8 / NW of them
+    // tokens, the rest weights (gate rows, then up rows)
+    constexpr int XQ = BM / 8 / S::NW, FQ = BF / 8 / S::NW;
+    const auto bytes_from = [&](int64_t rows, int64_t from, int64_t ld) {
+        return ((rows - 1 - from) * ld + a.K) * (int64_t)sizeof(E);
+    };
+    const __amdgpu_buffer_rsrc_t xbuf = panel(a.X + row0 * a.ldx, bytes_from(a.M, row0, a.ldx));
+    const __amdgpu_buffer_rsrc_t w0buf = panel(a.W0 + col0 * a.ldw, bytes_from(a.N, col0, a.ldw));
+    const __amdgpu_buffer_rsrc_t w1buf = GATED ? panel(a.W1 + col0 * a.ldw, bytes_from(a.N, col0, a.ldw)) : w0buf;
+    uint32_t off[S::PER_WAVE], chunk[S::PER_WAVE];
 #pragma unroll
     for (int q = 0; q < S::PER_WAVE; ++q) {
-        const int j = wave + q * S::NW;
-        const int r = 8 * j + (lane >> 3);
-        if (8 * j < BM) {
-            const int64_t t = row0 + r < a.M ? row0 + r : a.M - 1;
-            chunk[q] = (lane & 7) ^ ((r >> 1) & 7);
-            src[q] = reinterpret_cast<const char *>(a.X + t * a.ldx);
+        const int r = 8 * (wave + q * S::NW) + (lane >> 3);  // panel row
+        if (q < XQ) {
+            chunk[q] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+            off[q] = (uint32_t)r * (uint32_t)(a.ldx * sizeof(E)) + chunk[q];
         } else {
-            const int rw = r - BM;
-            const bool up = GATED && rw >= BF;
-            const int64_t n0 = col0 + (up ? rw - BF : rw);
-            const int64_t n = n0 < a.N ? n0 : a.N - 1;
-            chunk[q] = (lane & 7) ^ (((rw >> 1) & 1) | (((rw >> 3) & 3) << 1));
-            src[q] = reinterpret_cast<const char *>((up ? a.W1 : a.W0) + n * a.ldw);
+            const int rw = r - BM, f = q < XQ + FQ ? rw : rw - BF;
+            chunk[q] = 16 * ((lane & 7) ^ (((rw >> 1) & 1) | (((rw >> 3) & 3) << 1)));
+            off[q] = (uint32_t)f * (uint32_t)(a.ldw * sizeof(E)) + chunk[q];
         }
     }
-    const int64_t row_bytes = a.K * (int64_t)sizeof(E);
-    const int slices = (int)((row_bytes + 127) / 128);
-    auto issue = [&](int s) {
-        char *dst = smem + (s % NS) * S::STAGE;
-        const int64_t off = (int64_t)s * 128;
-        const bool whole = off + 128 <= row_bytes;
+    const int row_bytes = (int)(a.K * (int64_t)sizeof(E));
+    const int stages = (row_bytes + 128 * SL - 1) / (128 * SL);
+    auto issue = [&](int s) __attribute__((always_inline)) {
+        char *dst = smem + s % NS * S::STAGE;
 #pragma unroll
-        for (int q = 0; q < S::PER_WAVE; ++q) {
-            const int64_t o = off + 16 * chunk[q];
-            const void *p = whole || o < row_bytes ? (const void *)(src[q] + o) : (const void *)g_zero;
-            lds_dma16(p, dst + (wave + q * S::NW) * 1024);
+        for (int h = 0; h < SL; ++h) {
+            const int k = (s * SL + h) * 128, left = row_bytes - k;
+#pragma unroll
+            for (int q = 0; q < S::PER_WAVE; ++q)
+                buffer_to_lds16(q < XQ ? xbuf : q < XQ + FQ ? w0buf : w1buf, (int)chunk[q] < left ? off[q] : kOutside,
+                                (uint32_t)k, dst + h * S::SLAB + (wave + q * S::NW) * 1024);
         }
     };
 
@@ -100,18 +102,18 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
 #pragma unroll
         for (int j = 0; j < S::TN; ++j) acc[i][j] = f32x4{};
 
-    for (int p = 0; p < NS - 1 && p < slices; ++p) issue(p);
+#pragma unroll
+    for (int p = 0; p < NS - 1; ++p) issue(p);
     const int swx = (i16 >> 1) & 7, sww = ((i16 >> 1) & 1) | ((i16 >> 2) << 1);
     const int wrow = 8 * (i16 >> 2) + (i16 & 3);
-    for (int s = 0; s < slices; ++s) {
-        // all but the slices issued after s have landed; the barrier makes every
-        // wavefront's part visible and frees the buffer of slice s - 1
-        if (slices - 1 - s >= NS - 2) wait_vmcnt<(NS - 2) * S::PER_WAVE>();
-        else wait_vmcnt<0>();
+    for (int s = 0; s < stages; ++s) {
+        // all but the stages issued after s have landed; the barrier makes every
+        // wavefront's part visible and frees the buffer of stage s - 1
+        wait_vmcnt<(NS - 2) * SL * S::PER_WAVE>();
         barrier_only();
-        if (s + NS - 1 < slices) issue(s + NS - 1);
-        const char *sx = smem + (s % NS) * S::STAGE + (wm * S::TM * 16 + i16) * 128;
-        const char *sw = smem + (s % NS) * S::STAGE + (BM + wn * S::TF * 16 + wrow) * 128;
+        issue(s + NS - 1);
+        const char *sx = smem + s % NS * S::STAGE + (wm * S::TM * 16 + i16) * 128;
+        const char *sw = smem + s % NS * S::STAGE + (BM + wn * S::TF * 16 + wrow) * 128;
         typedef typename Frag<E>::type F;
         auto frag = [&](const char *row, int h, int swz) -> F {
             if constexpr (sizeof(E) == 2) {
@@ -122,22 +124,25 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
                 return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         };
+        constexpr int STEPS = 4 / (int)sizeof(E);  // 32-deep steps of a slab
 #pragma unroll
-        for (int h = 0; h < S::BK / 32; ++h) {
+        for (int hh = 0; hh < SL * STEPS; ++hh) {
+            const int slab = hh / STEPS * S::SLAB, h = hh % STEPS;
             F fw[S::TN], fx[S::TM];
 #pragma unroll
             for (int j = 0; j < S::TN; ++j) {
                 const int jf = j % S::TF;
-                fw[j] = frag(sw + ((j / S::TF) * BF + 32 * (jf >> 1) + 4 * (jf & 1)) * 128, h, sww);
+                fw[j] = frag(sw + slab + ((j / S::TF) * BF + 32 * (jf >> 1) + 4 * (jf & 1)) * 128, h, sww);
             }
 #pragma unroll
-            for (int i = 0; i < S::TM; ++i) fx[i] = frag(sx + i * 16 * 128, h, swx);
+            for (int i = 0; i < S::TM; ++i) fx[i] = frag(sx + slab + i * 16 * 128, h, swx);
 #pragma unroll
             for (int i = 0; i < S::TM; ++i)
 #pragma unroll
                 for (int j = 0; j < S::TN; ++j) acc[i][j] = mma32(acc[i][j], fw[j], fx[i]);
         }
     }
+    wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
     // ---- epilogue: 8 consecutive features of one token per pair of blocks
 #pragma unroll
     for (int p = 0; p < S::TF / 2; ++p) {
@@ -145,8 +150,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
         const int have = (int)std::min<int64_t>(8, a.N - c);
         if (have <= 0) continue;
         float b0[8] = {}, b1[8] = {};
-        if (a.b0) load_row(a.b0 + c, b0, false, have);
-        if (GATED && a.b1) load_row(a.b1 + c, b1, false, have);
+        if (a.b0) load_row(a.b0 + c, b0, have);
+        if (GATED && a.b1) load_row(a.b1 + c, b1, have);
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
             const int64_t t = row0 + (wm * S::TM + i) * 16 + i16;
@@ -160,37 +165,70 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
                 for (int q = 0; q < 8; ++q) v[q] *= acc[i][S::TF + 2 * p + (q >> 2)][q & 3] + b1[q];
             } else if (a.R) {
                 float r[8];
-                load_row(a.R + t * a.ldr + c, r, a.vec, have);
+                load_row(a.R + t * a.ldr + c, r, have);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] += r[q];
             }
-            store_row(a.Y + t * a.ldy + c, v, a.vec, have);
+            store_row(a.Y + t * a.ldy + c, v, have);
         }
     }
 }
 
-template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, bool GATED>
+template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED>
 hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BF - 1) / BF;
     const int64_t ntiles = tiles_m * tiles_n;
     if (ntiles > (int64_t)INT32_MAX - 8) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
-    hipLaunchKernelGGL((linear_tile_kernel<E, O, BM, BF, WM, WN, NS, GATED>), dim3((unsigned)(8 * per_xcd)),
+    hipLaunchKernelGGL((linear_tile_kernel<E, O, BM, BF, WM, WN, NS, SL, GATED>), dim3((unsigned)(8 * per_xcd)),
                        dim3(64 * WM * WN), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd);
     return hipGetLastError();
+}
+
+// Tile shapes by tokens and weight rows (gated: gate and up rows together), and
+// the time of a round of one tile per CU: per slab as measured for bf16 at K =
+// 4096 (ns; float32 is bound by its MFMAs above 2400 ns per 128 x 128), and for the
+// start and the epilogue.
+enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T256x256 };
+struct TileCost {
+    int bm, bn;
+    double slab, once;
+};
+constexpr TileCost kTiles[] = {{32, 64, 185, 3000},   {64, 64, 205, 3000},   {64, 128, 365, 3000},
+                               {128, 128, 560, 3000}, {128, 256, 920, 4500}, {256, 256, 1300, 6000}};
+
+// The shape with the smallest estimated time for a product of `rows` weight rows.
+template <typename E> Tile pick_tile(double M, double rows, double slabs) {
+    Tile best = T32x64;
+    double cost = 1e300;
+    for (int i = T32x64; i <= (sizeof(E) == 2 ? T256x256 : T128x128); ++i) {
+        const TileCost &t = kTiles[i];
+        const double rounds = std::ceil(std::ceil(M / t.bm) * std::ceil(rows / t.bn) / 256.0);
+        const double slab = sizeof(E) == 2 ? t.slab : std::max(t.slab, 2400.0 * t.bm * t.bn / 16384.0);
+        const double c = rounds * (slabs * slab + t.once);
+        if (c < cost) {
+            cost = c;
+            best = (Tile)i;
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
+    const Tile tile = pick_tile<E>((double)a.M, (double)a.N * (GATED ? 2 : 1), std::ceil((double)a.K * sizeof(E) / 128.0));
     if constexpr (sizeof(E) == 2) {
-        const int64_t t256 = ((a.M + 255) / 256) * ((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-        if (t256 >= 128 && big_strides(a)) return launch_big<O, GATED>(a, st);
+        if (tile == T256x256) return launch_big<O, GATED>(a, st);
+        if (tile == T128x256) return launch_tile<E, O, 128, GATED ? 128 : 256, 2, 4, 3, 1, GATED>(a, st);
     }
-    const int64_t big = ((a.M + 127) / 128) * ((a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
-    if (big >= 192) return launch_tile<E, O, 128, GATED ? 64 : 128, 2, 2, 2, GATED>(a, st);
-    return launch_tile<E, O, 64, GATED ? 32 : 64, 4, 1, 3, GATED>(a, st);
+    switch (tile) {
+    case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, 5, 2, GATED>(a, st);
+    case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, 4, 2, GATED>(a, st);
+    case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 5, 1, GATED>(a, st);
+    default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 4, 1, GATED>(a, st);
+    }
 }
 
 template hipError_t launch_linear<bf16, bf16, false>(const LinearArgs<bf16, bf16> &, hipStream_t);

@@ -28,8 +28,7 @@
 // 8 newer copies are outstanding, and the barrier after it publishes them.  A
 // wavefront's stores count among its copies and complete in order with them; up
 // to the first copy issued after an epilogue, the waits leave that epilogue's
-// stores outstanding too (when their number is known: whole tiles, 16-byte
-// stores).
+// stores outstanding too (when their number is known: whole tiles).
 //
 // Four phases of 16 MFMAs a slab, one per quadrant, took 811 us at 8192^3 where
 // two of 32 take 730 (1.51 PFLOP/s; the library's product 680).
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         }
         // ---- epilogue: 8 consecutive features of a token per pair of weight blocks
         const int el = fresh_lane(), ei = el & 15, eg = el >> 4;
-        stores_out = a.vec && row0 + BM <= a.M && col0 + BF <= a.N;
+        stores_out = row0 + BM <= a.M && col0 + BF <= a.N;
         constexpr int HW = GATED ? 1 : 2;
         int64_t c[HW];
         int have[HW];
@@ -242,8 +241,8 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         for (int hw = 0; hw < HW; ++hw) {
             c[hw] = col0 + (GATED ? 32 * wn : 64 * wn + 32 * hw) + 8 * eg;
             have[hw] = (int)min((int64_t)8, a.N - c[hw]);
-            if (a.b0) load_row(a.b0 + c[hw], b0[hw], false, have[hw]);
-            if (GATED && a.b1) load_row(a.b1 + c[hw], b1, false, have[hw]);
+            if (a.b0) load_row(a.b0 + c[hw], b0[hw], have[hw]);
+            if (GATED && a.b1) load_row(a.b1 + c[hw], b1, have[hw]);
         }
         // both halves of a row one after the other: whole 128-byte lines
 #pragma unroll
@@ -263,11 +262,11 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
                         for (int q = 0; q < 8; ++q) v[q] *= acc[hx][1][i][q >> 2][q & 3] + b1[q];
                     } else if (a.R) {
                         float r[8];
-                        load_row(a.R + t * a.ldr + c[hw], r, a.vec, have[hw]);
+                        load_row(a.R + t * a.ldr + c[hw], r, have[hw]);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) v[q] += r[q];
                     }
-                    store_row(a.Y + t * a.ldy + c[hw], v, a.vec, have[hw]);
+                    store_row(a.Y + t * a.ldy + c[hw], v, have[hw]);
                 }
             }
         tile += nslots;
@@ -279,15 +278,10 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
     wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
 }
 
-// A tile's 256 rows are addressed by 32-bit byte offsets below 2^31.
-template <typename O> bool big_strides(const LinearArgs<bf16, O> &a) {
-    return a.ldx < (int64_t)1 << 21 && a.ldw < (int64_t)1 << 21;
-}
-
 template <typename O, bool GATED> hipError_t launch_big(const LinearArgs<bf16, O> &a, hipStream_t st) {
     const int64_t tiles_m = (a.M + 255) / 256, tiles_n = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
     const int64_t ntiles = tiles_m * tiles_n;
-    if (ntiles > (int64_t)1 << 24 || !big_strides(a)) return hipErrorInvalidValue;
+    if (ntiles > (int64_t)1 << 24) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
     // one workgroup per CU: 32 on each XCD
     const int64_t slots = per_xcd < 32 ? per_xcd : 32;

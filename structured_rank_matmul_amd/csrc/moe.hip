@@ -27,79 +27,116 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
 
-template <typename E, int PER>  // PER values per lane: E_n <= 64 PER
+// v of the lane whose number differs in bit D of a group of LANES (16: by DPP,
+// inside a row of the wavefront; 64: across rows by LDS permute).
+template <int D> __device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);        // quad_perm 1 0 3 2
+    else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);   // quad_perm 2 3 0 1
+    else if constexpr (D == 4) return __shfl_xor(v, 4);
+    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true);  // row_ror 8
+    else return __shfl_xor(v, D);
+}
+template <int LANES, class F> __device__ __forceinline__ void butterfly(F &&f) {
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 8>{});
+    if constexpr (LANES == 64) {
+        f(std::integral_constant<int, 16>{});
+        f(std::integral_constant<int, 32>{});
+    }
+}
+template <int LANES> __device__ __forceinline__ float lane_sum(float v) {
+    butterfly<LANES>([&](auto d) __attribute__((always_inline)) {
+        v += __uint_as_float(lane_xor<decltype(d)::value>(__float_as_uint(v)));
+    });
+    return v;
+}
+
+// LANES lanes a row, PER consecutive values each (E_n <= LANES PER), as keys in
+// registers.  A round finds the largest key of a lane and of the lanes, and the
+// first lane and place that hold it; a taken key becomes 0.  Lane j keeps the j-th
+// choice (k <= LANES).  Few lanes a row cost few exchange steps.
+template <typename E, int LANES, int PER>
 __global__ __launch_bounds__(256) void route_kernel(const E *__restrict__ logits, int64_t ld, int64_t T, int En, int k,
                                                     bool sigmoid, bool renormalise, float scale,
                                                     int32_t *__restrict__ ids, float *__restrict__ w) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
-    const E *row = logits + t * ld;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x & 63 & ~(LANES - 1);
+    const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+    const int64_t t = row < T ? row : T - 1;  // whole wavefronts run; only rows of T are stored
+    const E *p = logits + t * ld + lane * PER;
+    const int have = En - lane * PER;
     float v[PER];
-    bool ok[PER];
+    if constexpr (PER * sizeof(E) % 16 == 0) {
+        load_row(p, v, have);
+    } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) v[q] = q < have ? to_f32(p[q]) : 0.f;
+    }
+    uint32_t key[PER], top = 0;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-        const int e = 64 * q + lane;
-        v[q] = e < En ? to_f32(row[e]) : -INFINITY;
-        ok[q] = v[q] > -INFINITY;  // false for NaN too
+        key[q] = q < have && v[q] > -INFINITY ? order_key(v[q]) : 0;  // 0 for NaN too
+        top = max(top, key[q]);
     }
-    unsigned taken = 0;
-    float mine = 0.f;  // lane j: the j-th chosen value and expert
-    int my_id = -1;
-    float top = 0.f;
-    for (int j = 0; j < k; ++j) {
-        uint32_t key = 0;
-        int at = En;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const uint32_t o = ok[q] && !((taken >> q) & 1u) ? order_key(v[q]) : 0;
-            if (o > key) {
-                key = o;
-                at = 64 * q + lane;
-            }
-        }
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-            const uint32_t ok2 = __shfl_xor(key, d);
-            const int at2 = __shfl_xor(at, d);
-            if (ok2 > key || (ok2 == key && at2 < at)) {
-                key = ok2;
-                at = at2;
-            }
-        }
-        if (key == 0) break;
-        if ((at & 63) == lane) taken |= 1u << (at >> 6);
-        const float val = __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-        if (j == 0) top = val;
-        if (lane == j) {
-            mine = val;
-            my_id = at;
-        }
-    }
-    float p = 0.f;
-    if (sigmoid) {
-        if (my_id >= 0) p = 1.f / (1.f + expf(-mine));
-    } else {
-        // exp(l - top), 1 where l == top (also at +inf)
-        float sum = 0.f;
+    butterfly<LANES>([&](auto d) __attribute__((always_inline)) { top = max(top, lane_xor<decltype(d)::value>(top)); });
+    const float largest = key_value(top);
+    float sum = 0.f;
+    if (!sigmoid) {  // exp(l - largest), 1 where l is the largest (also at +inf)
 #pragma unroll
         for (int q = 0; q < PER; ++q)
-            if (ok[q]) sum += v[q] == top ? 1.f : expf(v[q] - top);
+            if (key[q] != 0) sum += key[q] == top ? 1.f : expf(v[q] - largest);
+        sum = lane_sum<LANES>(sum);
+    }
+    uint32_t chosen = 0;
+    int at = -1;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-        if (my_id >= 0) p = (mine == top ? 1.f : expf(mine - top)) / sum;
+        for (int q = 1; q < PER; ++q) best = max(best, key[q]);
+        uint32_t all = best;
+        butterfly<LANES>([&](auto d) __attribute__((always_inline)) { all = max(all, lane_xor<decltype(d)::value>(all)); });
+        // the first lane that holds it (lanes hold rising indices), and its first place
+        const uint64_t holders = __ballot(best == all) >> group;
+        const int first = __ffsll((unsigned long long)holders) - 1;
+        int place = 0;
+#pragma unroll
+        for (int q = PER - 1; q >= 0; --q) place = key[q] == all ? q : place;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) key[q] = lane == first && q == place ? 0 : key[q];
+        const int index = __shfl(lane * PER + place, group + first);
+        if (lane == j) {
+            chosen = all;
+            at = all != 0 ? index : -1;
+        }
+    }
+    float weight = 0.f;
+    if (at >= 0) {
+        const float l = key_value(chosen);
+        weight = sigmoid ? 1.f / (1.f + expf(-l)) : (chosen == top ? 1.f : expf(l - largest)) / sum;
     }
     if (renormalise) {
-        float sum = p;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-        if (sum > 0.f) p /= sum;
+        const float total = lane_sum<LANES>(weight);
+        if (total > 0.f) weight /= total;
     }
-    if (lane < k) {
-        ids[t * k + lane] = my_id;
-        w[t * k + lane] = my_id >= 0 ? p * scale : 0.f;
+    if (row < T && lane < k) {
+        ids[t * k + lane] = at;
+        w[t * k + lane] = weight * scale;
     }
+}
+
+template <typename E, int LANES, int PER>
+hipError_t launch_route_lanes(const E *logits, int64_t ld, int64_t T, int En, int k, bool sigmoid, bool renormalise,
+                              float scale, int32_t *ids, float *w, hipStream_t st) {
+    const int64_t grid = (T + 256 / LANES - 1) / (256 / LANES);
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((route_kernel<E, LANES, PER>), dim3((unsigned)grid), dim3(256), 0, st, logits, ld, T, En, k,
+                       sigmoid, renormalise, scale, ids, w);
+    return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ expert layer
@@ -383,18 +420,13 @@ template <typename E>
 hipError_t launch_route(const E *logits, int64_t ld, int64_t T, int En, int k, bool sigmoid, bool renormalise,
                         float scale, int32_t *ids, float *w, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    const int64_t grid = (T + 3) / 4;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-#define DYRA_ROUTE(P)                                                                                              \
-    hipLaunchKernelGGL((route_kernel<E, P>), dim3((unsigned)grid), dim3(256), 0, st, logits, ld, T, En, k, sigmoid, \
-                       renormalise, scale, ids, w)
-    if (En <= 64) DYRA_ROUTE(1);
-    else if (En <= 128) DYRA_ROUTE(2);
-    else if (En <= 256) DYRA_ROUTE(4);
-    else if (En <= 512) DYRA_ROUTE(8);
-    else DYRA_ROUTE(16);
+    // 16 lanes a row where they hold its values (up to 16 each) and its choices
+#define DYRA_ROUTE(LANES, PER) \
+    launch_route_lanes<E, LANES, PER>(logits, ld, T, En, k, sigmoid, renormalise, scale, ids, w, st)
+    if (k <= 16 && En <= 256)
+        return En <= 32 ? DYRA_ROUTE(16, 2) : En <= 64 ? DYRA_ROUTE(16, 4) : En <= 128 ? DYRA_ROUTE(16, 8) : DYRA_ROUTE(16, 16);
+    return En <= 256 ? DYRA_ROUTE(64, 4) : En <= 512 ? DYRA_ROUTE(64, 8) : DYRA_ROUTE(64, 16);
 #undef DYRA_ROUTE
-    return hipGetLastError();
 }
 
 template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st) {

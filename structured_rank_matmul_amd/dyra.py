@@ -430,7 +430,14 @@ def _input(X, name="X"):
     if dev < 0:
         raise ValueError("tensor must be on the GPU")
     rows, cols = X.shape
-    return rows, cols, _matrix(X, name, dev, rows, cols, X.dtype), dev
+    ld, step = X.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    if rows <= 1:
+        ld = cols
+    elif ld == 0:
+        raise ValueError(f"{name} must not repeat one row")
+    return rows, cols, ld, dev
 
 
 def _matrix(t, name, dev, rows, cols, dtype, broadcast=False) -> int:
@@ -457,24 +464,31 @@ def _whole(t, name, dev, shape, dtype) -> int:
 
 
 def _new(shape, dtype, X, stream):
-    t = X.new_empty(shape) if dtype == X.dtype else X.new_empty(shape, dtype=dtype)
+    t = X.new_empty(shape, dtype=dtype)
     if stream is not None:
         _on_stream(t, stream)
     return t
 
 
+_cuda = None   # torch's current device and current raw stream of a device
+
+
 def _run(fn, what, dev, stream, *args) -> None:
     """fn(*args, stream) with device `dev` current, so that the stream and the launch agree."""
-    import torch
+    global _cuda
+    if _cuda is None:
+        import torch
+        _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(dev)
+        st = _cuda[1](dev)
     elif stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {dev}")
     else:
         st = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _cuda[0]() == dev:
         status = fn(*args, st)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, st)
     if status != 0:

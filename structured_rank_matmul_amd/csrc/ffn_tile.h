@@ -110,21 +110,67 @@ template <typename T, int N> __device__ __forceinline__ void load_row(const T *p
         for (int q = 0; q < N; ++q) v[q] = q < have ? to_f32(p[q]) : 0.f;
     }
 }
-template <typename T, int N> __device__ __forceinline__ void store_row(T *p, const float (&v)[N], int have) {
-    constexpr int V = 16 / (int)sizeof(T);
-    if (have >= N) {
+// Eight elements of a residual row in flight: requested for a batch of rows before
+// the first is used (loads used one by one cost each its latency).
+template <typename T> struct Residual8 {
+    u32x4 c[8 * (int)sizeof(T) / 16];
+    __device__ __forceinline__ void request(const T *p) {
 #pragma unroll
-        for (int q = 0; q < N; q += V) {
-            union { u32x4 u; T e[V]; } w;
-#pragma unroll
-            for (int i = 0; i < V; ++i) w.e[i] = to_elem<T>(v[q + i]);
-            *reinterpret_cast<u32x4_any *>(p + q) = w.u;
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-            if (q < have) p[q] = to_elem<T>(v[q]);
+        for (int q = 0; q < 8 * (int)sizeof(T) / 16; ++q) c[q] = *reinterpret_cast<const u32x4_any *>((const char *)p + 16 * q);
     }
+    __device__ __forceinline__ void add_to(float (&v)[8]) const {
+        union { u32x4 u[8 * sizeof(T) / 16]; T e[8]; } w;
+#pragma unroll
+        for (int q = 0; q < 8 * (int)sizeof(T) / 16; ++q) w.u[q] = c[q];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += to_f32(w.e[q]);
+    }
+};
+// The same of a row of which the first `have` (0 .. 8) exist; columns past them
+// repeat the last one and are not stored.
+template <typename T> __device__ __forceinline__ void add_row(float (&v)[8], const T *p, int have) {
+    if (have >= 8) {
+        Residual8<T> r;
+        r.request(p);
+        r.add_to(v);
+    } else if (have > 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += to_f32(p[q < have ? q : have - 1]);
+    }
+}
+// Eight results of a row, of which the first `have` (0 .. 8) exist: a 16-byte store (two
+// for float32), or, in the last columns, one each of four, two and one element.
+__device__ __forceinline__ void store_row(float *p, const float (&v)[8], int have) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef f32x4 f32x4_any __attribute__((aligned(4)));
+    typedef f32x2 f32x2_any __attribute__((aligned(4)));
+    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    const bool four = have & 4, two = have & 2;
+    if (have >= 8 || four) *reinterpret_cast<f32x4_any *>(p) = lo;
+    if (have >= 8) {
+        *reinterpret_cast<f32x4_any *>(p + 4) = hi;
+        return;
+    }
+    const f32x4 rest = four ? hi : lo;
+    if (two) *reinterpret_cast<f32x2_any *>(p + (have & 4)) = f32x2{rest[0], rest[1]};
+    if (have & 1) p[have & 6] = two ? rest[2] : rest[0];
+}
+__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[8], int have) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 u32x2_any __attribute__((aligned(2)));
+    typedef unsigned u32_any __attribute__((aligned(2)));
+    union { u32x4 u; bf16 e[8]; } w;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w.e[q] = to_elem<bf16>(v[q]);
+    if (have >= 8) {
+        *reinterpret_cast<u32x4_any *>(p) = w.u;
+        return;
+    }
+    const bool four = have & 4, two = have & 2;
+    if (four) *reinterpret_cast<u32x2_any *>(p) = u32x2{w.u[0], w.u[1]};
+    if (two) *reinterpret_cast<u32_any *>(p + (have & 4)) = four ? w.u[2] : w.u[0];
+    const unsigned last = four ? (two ? w.u[3] : w.u[2]) : (two ? w.u[1] : w.u[0]);
+    if (have & 1) *reinterpret_cast<unsigned short *>(p + (have & 6)) = (unsigned short)last;
 }
 
 }  // namespace dyra

@@ -152,6 +152,13 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
         float b0[8] = {}, b1[8] = {};
         if (a.b0) load_row(a.b0 + c, b0, have);
         if (GATED && a.b1) load_row(a.b1 + c, b1, have);
+        const bool ahead = !GATED && a.R && have >= 8;
+        Residual8<O> r[S::TM];
+        if (ahead) {
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+                r[i].request(a.R + std::min<int64_t>(row0 + (wm * S::TM + i) * 16 + i16, a.M - 1) * a.ldr + c);
+        }
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
             const int64_t t = row0 + (wm * S::TM + i) * 16 + i16;
@@ -163,11 +170,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
             if constexpr (GATED) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= acc[i][S::TF + 2 * p + (q >> 2)][q & 3] + b1[q];
+            } else if (ahead) {
+                r[i].add_to(v);
             } else if (a.R) {
-                float r[8];
-                load_row(a.R + t * a.ldr + c, r, have);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] += r[q];
+                add_row(v, a.R + t * a.ldr + c, have);
             }
             store_row(a.Y + t * a.ldy + c, v, have);
         }
@@ -189,13 +195,14 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
 // the time of a round of one tile per CU: per slab as measured for bf16 at K =
 // 4096 (ns; float32 is bound by its MFMAs above 2400 ns per 128 x 128), and for the
 // start and the epilogue.
-enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T256x256 };
+enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T192x256, T224x256, T256x256 };
 struct TileCost {
     int bm, bn;
     double slab, once;
 };
 constexpr TileCost kTiles[] = {{32, 64, 185, 3000},   {64, 64, 205, 3000},   {64, 128, 365, 3000},
-                               {128, 128, 560, 3000}, {128, 256, 920, 4500}, {256, 256, 1300, 6000}};
+                               {128, 128, 560, 3000}, {128, 256, 920, 4500}, {192, 256, 1060, 5000},
+                               {224, 256, 1180, 5500}, {256, 256, 1300, 6000}};
 
 // The shape with the smallest estimated time for a product of `rows` weight rows.
 template <typename E> Tile pick_tile(double M, double rows, double slabs) {
@@ -220,7 +227,9 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
     const Tile tile = pick_tile<E>((double)a.M, (double)a.N * (GATED ? 2 : 1), std::ceil((double)a.K * sizeof(E) / 128.0));
     if constexpr (sizeof(E) == 2) {
-        if (tile == T256x256) return launch_big<O, GATED>(a, st);
+        if (tile == T256x256) return launch_big<O, GATED, 8>(a, st);
+        if (tile == T224x256) return launch_big<O, GATED, 7>(a, st);
+        if (tile == T192x256) return launch_big<O, GATED, 6>(a, st);
         if (tile == T128x256) return launch_tile<E, O, 128, GATED ? 128 : 256, 2, 4, 3, 1, GATED>(a, st);
     }
     switch (tile) {

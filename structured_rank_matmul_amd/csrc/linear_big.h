@@ -1,10 +1,13 @@
-// 256 x 256 tiles of the linear layer and the gated pair, bf16, for products
+// 256 x 256 tiles (224 and 192 x 256 too) of the linear layer and the gated pair, bf16, for products
 // that fill the chip: eight wavefronts in two groups of four that take turns on
 // the matrix cores.
 //
-// A workgroup owns 256 tokens and 256 weight rows (256 output features, or 128
-// gate and the same 128 up rows).  Wavefront (wm, wn) owns tokens 128 wm .. and
-// 64 weight rows: 128 accumulator registers.  K advances in slabs of 64 (128
+// A workgroup owns 32 TB tokens and 256 weight rows (256 output features, or 128
+// gate and the same 128 up rows).  Wavefront (wm, wn) owns TB blocks of 16 tokens
+// (4 in half A, the rest in half B) and 64 weight rows: 16 TB accumulator
+// registers.  TB is 8; 7 and 6 serve products that the lower tiles divide into
+// fewer or smaller rounds of one tile per CU (their panel keeps 128 rows per wm,
+// the last ones empty).  K advances in slabs of 64 (128
 // bytes per row) through two LDS buffers.  A slab is two phases, one per half of
 // the wavefront's tokens, 32 MFMAs each:
 //
@@ -48,13 +51,13 @@ __device__ __forceinline__ int fresh_lane() {
     return l;
 }
 
-template <typename O, bool GATED>
+template <typename O, bool GATED, int TB>
 __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> a, int tiles_m, int tiles_n,
                                                             int per_xcd) {
-    constexpr int BM = 256, BF = GATED ? 128 : 256;
+    constexpr int BM = 32 * TB, BF = GATED ? 128 : 256;
     constexpr int STAGE = 32768, WOFF = 65536;  // two buffers of 256 token rows of 128 bytes, two of 256 weight rows
     // 16-byte stores of a wavefront's epilogue
-    constexpr int STORES = (GATED ? 1 : 2) * 8 * (8 * (int)sizeof(O) / 16);
+    constexpr int STORES = (GATED ? 1 : 2) * TB * (8 * (int)sizeof(O) / 16);
     __shared__ __align__(16) char smem[4 * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -95,7 +98,8 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                xoff[h][q] = (uint32_t)min(128 * q + 64 * h + 8 * wave + lr, tmax) * xld + xchunk;
+                const int r = 64 * h + 8 * wave + lr;  // of the 128 that the panel has for wm = q
+                xoff[h][q] = r < 16 * TB ? (uint32_t)min(16 * TB * q + r, tmax) * xld + xchunk : kOutside;
                 const int b = wave + 8 * q;
                 const int f = (GATED ? 32 : 64) * (b >> 2) + (GATED ? 0 : 32 * h) + 8 * (b & 3) + lr;
                 woff[h][q] = (uint32_t)min(f, fmax) * wld + wchunk;
@@ -147,7 +151,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < (h == 0 ? 4 : TB - 4); ++i)
                 fx[k][i] = *reinterpret_cast<const bf16x8 *>(p + 16 * i * 128 + (((4 * k + g) ^ swx) << 4));
     };
     auto read_w = [&](int h, int buf, int slot) __attribute__((always_inline)) {
@@ -168,7 +172,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < (hx == 0 ? 4 : TB - 4); ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         acc[hx][hw][i][j] = mma32(acc[hx][hw][i][j], fw[hw ? slot_b : slot_a][k][j], fx[k][i]);
@@ -230,45 +234,72 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
             slab(ic<1>{}, stores_out);
             stores_out = false;
         }
-        // ---- epilogue: 8 consecutive features of a token per pair of weight blocks
+        // ---- epilogue: 8 consecutive features of a token per pair of weight blocks.
+        // Whole tiles run a copy of the code made for their activation, without
+        // guards. One copy for everything, with branches over what a call does not
+        // use, took 181 us (no epilogue) and 195 us (bias and residual) at 25728 x
+        // 4096 -> 1024; this takes 175 and 187 (the library's bare product 169).
         const int el = fresh_lane(), ei = el & 15, eg = el >> 4;
-        stores_out = row0 + BM <= a.M && col0 + BF <= a.N;
+        const bool whole = row0 + BM <= a.M && col0 + BF <= a.N;
+        stores_out = whole;
         constexpr int HW = GATED ? 1 : 2;
-        int64_t c[HW];
-        int have[HW];
+        const int64_t c = col0 + (GATED ? 32 : 64) * wn + 8 * eg;  // hw = 1: 32 on
         float b0[HW][8] = {}, b1[8] = {};
 #pragma unroll
-        for (int hw = 0; hw < HW; ++hw) {
-            c[hw] = col0 + (GATED ? 32 * wn : 64 * wn + 32 * hw) + 8 * eg;
-            have[hw] = (int)min((int64_t)8, a.N - c[hw]);
-            if (a.b0) load_row(a.b0 + c[hw], b0[hw], have[hw]);
-            if (GATED && a.b1) load_row(a.b1 + c[hw], b1, have[hw]);
-        }
-        // both halves of a row one after the other: whole 128-byte lines
+        for (int hw = 0; hw < HW; ++hw)
+            if (a.b0) load_row(a.b0 + c + 32 * hw, b0[hw], whole ? 8 : (int)(a.N - c) - 32 * hw);
+        if (GATED && a.b1) load_row(a.b1 + c, b1, whole ? 8 : (int)(a.N - c));
+        // ACT below 0: of the call, with guards
+        auto finish = [&](auto act, auto residual) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+            constexpr bool RESIDUAL = decltype(residual)::value;
+            // rows whose residual is in flight together: what registers allow
+            constexpr int BATCH = RESIDUAL && ACT >= 0 ? (TB == 8 ? 2 : 4) * 2 / (int)sizeof(O) : 1;
+            const int64_t first = row0 + 16 * TB * wm + ei;
+            // both halves of a row one after the other: whole 128-byte lines
 #pragma unroll
-        for (int hx = 0; hx < 2; ++hx)
+            for (int i0 = 0; i0 < TB; i0 += BATCH) {
+                Residual8<O> r[BATCH][HW];
+                if constexpr (RESIDUAL && ACT >= 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t t = row0 + 128 * wm + 64 * hx + 16 * i + ei;
-                if (t >= a.M) continue;
+                    for (int i = i0; i < i0 + BATCH && i < TB; ++i)
 #pragma unroll
-                for (int hw = 0; hw < HW; ++hw) {
-                    float v[8];
+                        for (int hw = 0; hw < HW; ++hw) r[i - i0][hw].request(a.R + (first + 16 * i) * a.ldr + c + 32 * hw);
+                }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = acc[hx][hw][i][q >> 2][q & 3] + b0[hw][q];
-                    activate<sizeof(O) == 4>(v, a.act);
-                    if constexpr (GATED) {
+                for (int i = i0; i < i0 + BATCH && i < TB; ++i) {
+                    const int64_t t = first + 16 * i;
+                    if (ACT < 0 && t >= a.M) continue;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] *= acc[hx][1][i][q >> 2][q & 3] + b1[q];
-                    } else if (a.R) {
-                        float r[8];
-                        load_row(a.R + t * a.ldr + c[hw], r, have[hw]);
+                    for (int hw = 0; hw < HW; ++hw) {
+                        const int have = ACT >= 0 ? 8 : (int)max((int64_t)0, min((int64_t)8, a.N - c - 32 * hw));
+                        float v[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] += r[q];
+                        for (int q = 0; q < 8; ++q) v[q] = acc[i >> 2][hw][i & 3][q >> 2][q & 3] + b0[hw][q];
+                        activate<sizeof(O) == 4>(v, ACT >= 0 ? ACT : a.act);
+                        if constexpr (GATED) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) v[q] *= acc[i >> 2][1][i & 3][q >> 2][q & 3] + b1[q];
+                        }
+                        if constexpr (RESIDUAL && ACT >= 0) r[i - i0][hw].add_to(v);
+                        else if constexpr (RESIDUAL) add_row(v, a.R + t * a.ldr + c + 32 * hw, have);
+                        store_row(a.Y + t * a.ldy + c + 32 * hw, v, have);
                     }
-                    store_row(a.Y + t * a.ldy + c[hw], v, have[hw]);
                 }
             }
+        };
+        auto finish_act = [&](auto act) __attribute__((always_inline)) {
+            if constexpr (!GATED) {
+                if (a.R) return finish(act, std::true_type{});
+            }
+            finish(act, std::false_type{});
+        };
+        if (!whole) finish_act(ic<-1>{});
+        else if (a.act == kActNone) finish_act(ic<kActNone>{});
+        else if (a.act == kActRelu) finish_act(ic<kActRelu>{});
+        else if (a.act == kActGelu) finish_act(ic<kActGelu>{});
+        else if (a.act == kActGeluTanh) finish_act(ic<kActGeluTanh>{});
+        else finish_act(ic<kActSilu>{});
         tile += nslots;
         if (tile >= band_end) break;
         row0 = next_row0;
@@ -278,14 +309,14 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
     wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
 }
 
-template <typename O, bool GATED> hipError_t launch_big(const LinearArgs<bf16, O> &a, hipStream_t st) {
-    const int64_t tiles_m = (a.M + 255) / 256, tiles_n = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+template <typename O, bool GATED, int TB> hipError_t launch_big(const LinearArgs<bf16, O> &a, hipStream_t st) {
+    const int64_t tiles_m = (a.M + 32 * TB - 1) / (32 * TB), tiles_n = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
     const int64_t ntiles = tiles_m * tiles_n;
     if (ntiles > (int64_t)1 << 24) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
     // one workgroup per CU: 32 on each XCD
     const int64_t slots = per_xcd < 32 ? per_xcd : 32;
-    hipLaunchKernelGGL((linear_big_kernel<O, GATED>), dim3((unsigned)(8 * slots)), dim3(512), 0, st, a, (int)tiles_m,
+    hipLaunchKernelGGL((linear_big_kernel<O, GATED, TB>), dim3((unsigned)(8 * slots)), dim3(512), 0, st, a, (int)tiles_m,
                        (int)tiles_n, (int)per_xcd);
     return hipGetLastError();
 }

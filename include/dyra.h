@@ -307,7 +307,7 @@ dyra_status dyra_dense_ref(const void *X, const void *Wt, int64_t N, int64_t c1,
  * to the current device and to the device of the pointers, allocates nothing
  * and does not synchronise, so it may be captured into a graph.  An output must
  * not overlap an input, except that Y may be the residual itself (same pointer
- * and row stride).
+ * and row stride); an output at the address of another input is DYRA_ERR_ARG.
  */
 typedef enum {
     DYRA_ACT_NONE = 0,
@@ -331,9 +331,9 @@ typedef enum {
  *           they are.
  * dtype     DYRA_BF16 with out_dtype DYRA_BF16 or DYRA_F32, or DYRA_F32 with
  *           out_dtype DYRA_F32 (DYRA_ERR_DTYPE otherwise).
- * N >= 0 (0 is a no-op); N, c2 <= 2^30, c1, ldx, ldw <= 2^20.  X, Wt and their row strides are
- * 16-byte aligned, the others aligned to their elements (DYRA_ERR_ALIGN); a row
- * stride below the row's length is DYRA_ERR_ARG.
+ * N >= 0 (0 is a no-op); N, c2 <= 2^25, c1, ldx, ldw <= 2^20 (DYRA_ERR_SHAPE).
+ * X, Wt and their row strides are 16-byte aligned, the others aligned to their
+ * elements (DYRA_ERR_ALIGN); a row stride below the row's length is DYRA_ERR_ARG.
  */
 dyra_status dyra_linear(const void *X, int64_t ldx, const void *Wt, int64_t ldw, int64_t N, int64_t c1,
                         int64_t c2, dyra_dtype dtype, const void *bias, dyra_act act, const void *residual,
@@ -364,7 +364,8 @@ typedef enum {
  * A logit of -inf (a masked expert) or NaN is never chosen and adds nothing to
  * the softmax; places that are left over hold the id -1 and the weight 0, so a
  * row with every expert masked is all -1.  Experts at +inf share the softmax.
- * 1 <= topk <= min(experts, 64), experts <= 1024 (DYRA_ERR_SHAPE otherwise).
+ * 1 <= topk <= min(experts, 64), experts <= 1024, T <= 2^25 (DYRA_ERR_SHAPE
+ * otherwise).
  */
 dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t experts, int32_t topk,
                        dyra_dtype dtype, dyra_score score, int32_t renormalise, float scale, int32_t *ids,
@@ -383,7 +384,7 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
  * weights   device float32 [T][topk].
  * residual  device, dtype, [T][c], or NULL; ldr = 0 adds the same row to every
  *           token.
- * Y         device, dtype, [T][c].
+ * Y         device, dtype, [T][c]; may be the residual, and X too.
  * workspace device, >= dyra_moe_workspace_bytes(T, topk, f, dtype) bytes,
  *           contents on entry ignored; calls that overlap in time need separate
  *           ones.  It holds the experts' inner activations in dtype.

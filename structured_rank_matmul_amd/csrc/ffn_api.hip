@@ -11,7 +11,9 @@ namespace {
 
 using dyra::bf16;
 
-constexpr int64_t kMaxDim = int64_t{1} << 30;  // tokens, output features
+// Tokens, output features: the launches of any such sizes whose outputs fit the
+// card have less than 2^32 threads.
+constexpr int64_t kMaxDim = int64_t{1} << 25;
 // Elements of a row of X or of a weight, and between rows: the kernels address
 // the rows of a tile by 32-bit byte offsets from its first.
 constexpr int64_t kMaxRow = int64_t{1} << 20;
@@ -26,6 +28,13 @@ bool aligned(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 bool known(dyra_dtype t) { return t == DYRA_BF16 || t == DYRA_F32; }
 size_t size_of(dyra_dtype t) { return t == DYRA_BF16 ? 2 : 4; }
 bool known_act(dyra_act a) { return a >= DYRA_ACT_NONE && a <= DYRA_ACT_SILU; }
+
+// Whether Y of several rows is also an input that other rows' results still
+// read: X, a weight, or a residual whose rows lie otherwise.
+bool overlaps(const void *Y, int64_t ldy, int64_t N, const void *X, const void *W0, const void *W1, const void *R,
+              int64_t ldr) {
+    return Y == X || Y == W0 || Y == W1 || (R == Y && N > 1 && ldr != ldy);
+}
 
 // The checks that the linear layer and the gated pair share.  DYRA_OK with
 // *empty set: nothing to do.
@@ -78,6 +87,7 @@ dyra_status dyra_linear(const void *X, int64_t ldx, const void *Wt, int64_t ldw,
     if (residual && ldr != 0 && ldr < c2) return DYRA_ERR_ARG;
     if (empty) return DYRA_OK;
     if (!aligned(residual, size_of(out_dtype))) return DYRA_ERR_ALIGN;
+    if (overlaps(Y, ldy, N, X, Wt, Wt, residual, ldr)) return DYRA_ERR_ARG;
     if (!residual) ldr = 0;
     if (dtype == DYRA_F32)
         return run_linear<float, float, false>(X, ldx, Wt, nullptr, ldw, N, c1, c2, bias, nullptr, act, residual, ldr, Y, ldy, stream);
@@ -92,6 +102,7 @@ dyra_status dyra_gated(const void *X, int64_t ldx, const void *Wg, const void *W
     bool empty;
     const dyra_status s = check_linear(X, ldx, Wg, Wu, ldw, N, c1, c2, dtype, bias_g, bias_u, act, H, ldh, dtype, &empty);
     if (s != DYRA_OK || empty) return s;
+    if (overlaps(H, ldh, N, X, Wg, Wu, nullptr, 0)) return DYRA_ERR_ARG;
     if (dtype == DYRA_F32)
         return run_linear<float, float, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
     return run_linear<bf16, bf16, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
@@ -140,6 +151,10 @@ dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f
         return DYRA_ERR_ALIGN;
     if (!workspace || workspace_bytes < dyra_moe_workspace_bytes(T, topk, f, dtype)) return DYRA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return DYRA_ERR_ALIGN;
+    // Y over X is fine: X is read for the last time before Y is first written
+    if (overlaps(Y, ldy, T, nullptr, Wg, Wu, residual, ldr) || Y == Wd || workspace == Y || workspace == X ||
+        (workspace == residual))
+        return DYRA_ERR_ARG;
     hipStream_t st = (hipStream_t)stream;
     auto go = [&](auto e) {
         typedef decltype(e) E;

@@ -31,7 +31,7 @@ template <typename E, typename O> struct LinearArgs {
 };
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st);
-// Few tokens: the weights are streamed once per group of at most 64 tokens.
+// Few tokens: the weights are streamed once.
 template <typename E, typename O, bool GATED> hipError_t launch_skinny(const LinearArgs<E, O> &a, hipStream_t st);
 
 // Router: the k largest of every row of logits.

@@ -104,3 +104,27 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         dyra.dyra_moe(x, torch.zeros(2, 16, 64), torch.zeros(2, 16, 64), torch.zeros(2, 64, 16),
                       torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1))
+
+
+Q = 1 << 30   # addresses of their own
+APART = dict(X=Q, Wt=2 * Q, Y=3 * Q)
+
+
+@pytest.mark.parametrize("kw", [dict(Y=Q), dict(Y=2 * Q), dict(res=3 * Q, ldr=56), dict(res=3 * Q, ldr=0)])
+def test_linear_refuses_an_output_over_another_input(kw):
+    assert linear(**{**APART, **kw}) == ARG
+
+
+def test_gated_and_experts_refuse_an_output_over_another_input():
+    for h in (Q, 2 * Q, 3 * Q):
+        assert gated(X=Q, Wg=2 * Q, Wu=3 * Q, H=h) == ARG
+    apart = dict(X=Q, Wg=2 * Q, Wu=3 * Q, Wd=4 * Q, Y=5 * Q, ws=6 * Q)
+    for kw in (dict(Y=2 * Q), dict(Y=3 * Q), dict(Y=4 * Q), dict(ws=5 * Q), dict(ws=Q), dict(res=5 * Q, ldr=72),
+               dict(res=6 * Q, ldr=64)):
+        assert moe(**{**apart, **kw}) == ARG
+
+
+@pytest.mark.parametrize("kw", [dict(N=(1 << 25) + 1), dict(c2=(1 << 25) + 1, ldy=1 << 26), dict(c1=(1 << 20) + 8, ldx=1 << 21)])
+def test_sizes_past_the_limits(kw):
+    assert linear(**{**APART, **kw}) == SHAPE
+    assert route(T=(1 << 25) + 1) == SHAPE

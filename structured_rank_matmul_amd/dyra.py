@@ -464,9 +464,17 @@ def _whole(t, name, dev, shape, dtype) -> int:
 
 
 def _new(shape, dtype, X, stream):
-    t = X.new_empty(shape, dtype=dtype)
-    if stream is not None:
-        _on_stream(t, stream)
+    """An output or workspace.  Memory for another stream than the current one comes from that stream's pool (of
+    the current one's, work still pending there may write to it) and is kept from reuse until both are done with it."""
+    if stream is None:
+        return X.new_empty(shape, dtype=dtype)
+    import torch
+    current = torch.cuda.current_stream(X.device)
+    if stream == current or stream.device != X.device:
+        return X.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = X.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
     return t
 
 

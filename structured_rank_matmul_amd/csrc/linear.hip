@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E,
 #pragma unroll
             for (int q = 0; q < S::PER_WAVE; ++q)
                 buffer_to_lds16(q < XQ ? xbuf : q < XQ + FQ ? w0buf : w1buf, (int)chunk[q] < left ? off[q] : kOutside,
-                                (uint32_t)k, dst + h * S::SLAB + (wave + q * S::NW) * 1024);
+                                left > 0 ? (uint32_t)k : 0u, dst + h * S::SLAB + (wave + q * S::NW) * 1024);
         }
     };
 
@@ -192,17 +192,20 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
 }
 
 // Tile shapes by tokens and weight rows (gated: gate and up rows together), and
-// the time of a round of one tile per CU: per slab as measured for bf16 at K =
-// 4096 (ns; float32 is bound by its MFMAs above 2400 ns per 128 x 128), and for the
-// start and the epilogue.
+// the time of a round of one tile per CU: per slab (ns; from products of one and
+// of four full rounds at K = 1024 and 4096, bf16; float32 is bound by its MFMAs
+// above 2400 ns per 128 x 128), and for the start and the epilogue.  What the
+// choice is worth, us by tile (128 x 256 | 192 | 224 | 256 x 256): 448 363 333 336 at
+// 14336 x 4096 -> 4096, 388 307 306 276 at 12288, 237 212 173 181 at 25728 x 4096 ->
+// 1024, 62 62 65 71 at 2048 x 4096 -> 4096 (the library's product: 330, 265, 166, 55).
 enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T192x256, T224x256, T256x256 };
 struct TileCost {
     int bm, bn;
     double slab, once;
 };
-constexpr TileCost kTiles[] = {{32, 64, 185, 3000},   {64, 64, 205, 3000},   {64, 128, 365, 3000},
-                               {128, 128, 560, 3000}, {128, 256, 920, 4500}, {192, 256, 1060, 5000},
-                               {224, 256, 1180, 5500}, {256, 256, 1300, 6000}};
+constexpr TileCost kTiles[] = {{32, 64, 180, 2300},    {64, 64, 240, 2300},    {64, 128, 340, 3000},
+                               {128, 128, 560, 3500},  {128, 256, 920, 3800},  {192, 256, 1110, 4000},
+                               {224, 256, 1220, 5000}, {256, 256, 1340, 6000}};
 
 // The shape with the smallest estimated time for a product of `rows` weight rows.
 template <typename E> Tile pick_tile(double M, double rows, double slabs) {

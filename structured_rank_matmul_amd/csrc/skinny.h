@@ -101,6 +101,7 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
     __device__ __forceinline__ void issue(const SlabRows &w, uint32_t k, int left) { issue(w, w, k, left); }
     __device__ __forceinline__ void issue(const SlabRows &w, const SlabRows &x, uint32_t k, int left) {
         char *dst = ring + at * SLAB;
+        if (left <= 0) k = 0;  // past a short buffer's end the range check could wrap
         copy<WROWS>(w, k, left, dst);
         if constexpr (XROWS > 0) copy<XROWS>(x, k, left, dst + WBYTES);
         at = at + 1 == DEPTH ? 0 : at + 1;

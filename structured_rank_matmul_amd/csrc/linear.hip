@@ -7,9 +7,9 @@
 // A workgroup owns BM tokens x BF output features (gated: BF features of both
 // products, so a lane holds a feature's gate and up sums together and the
 // pair never reaches memory).  K advances in stages of SL slabs of 128 bytes per
-// row, copied from global memory straight into LDS, NS stages in flight (100 to
-// 144 KB: with one tile per CU, depth is what hides the latency), one barrier per
-// stage.  A slab row is 8 chunks of 16 bytes, chunk c at position c ^ sw(row), so
+// row, copied from global memory straight into LDS, NS stages in flight (for bf16
+// 100 to 144 KB: with one tile per CU, depth is what hides the latency), one
+// barrier per stage.  A slab row is 8 chunks of 16 bytes, chunk c at position c ^ sw(row), so
 // that the 16 rows a 16-lane group reads fall on distinct banks; the swizzle is
 // applied by choosing which chunk each lane of the copy fetches.  Rows past the
 // end, chunks past K and stages past the last are read out of the buffers'
@@ -39,12 +39,13 @@ template <typename E, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED
     static constexpr int PER_WAVE = (BM + BN) / 8 / NW;  // 1 KB copies of a slab
     static constexpr int SLAB = (BM + BN) * 128, STAGE = SL * SLAB;
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0 && BF / 8 % NW == 0, "whole copies per panel");
+    static constexpr int PER_CU = NS * STAGE <= 80 * 1024 ? 2 : 1;  // workgroups
     static_assert(TF % 2 == 0 && TM >= 1 && BF % 32 == 0 && NS * STAGE <= 160 * 1024, "tile shape");
 };
 
 template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles,
-                                                                   int per_xcd) {
+__global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL, GATED>::PER_CU * WM * WN / 4)) void linear_tile_kernel(
+    LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
     using S = TileShape<E, BM, BF, WM, WN, NS, SL, GATED>;
     __shared__ __align__(16) char smem[NS * S::STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -192,20 +193,20 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
 }
 
 // Tile shapes by tokens and weight rows (gated: gate and up rows together), and
-// the time of a round of one tile per CU: per slab (ns; from products of one and
-// of four full rounds at K = 1024 and 4096, bf16; float32 is bound by its MFMAs
-// above 2400 ns per 128 x 128), and for the start and the epilogue.  What the
+// the time of a round of one tile per CU: per slab in bf16 and in float32 (ns; from
+// products of one and of four full rounds at K = 1024 and 4096; a slab is 64 bf16 or
+// 32 floats), and for the start and the epilogue.  What the
 // choice is worth, us by tile (128 x 256 | 192 | 224 | 256 x 256): 448 363 333 336 at
 // 14336 x 4096 -> 4096, 388 307 306 276 at 12288, 237 212 173 181 at 25728 x 4096 ->
 // 1024, 62 62 65 71 at 2048 x 4096 -> 4096 (the library's product: 330, 265, 166, 55).
 enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T192x256, T224x256, T256x256 };
 struct TileCost {
     int bm, bn;
-    double slab, once;
+    double slab, slab_f32, once;
 };
-constexpr TileCost kTiles[] = {{32, 64, 180, 2300},    {64, 64, 240, 2300},    {64, 128, 340, 3000},
-                               {128, 128, 560, 3500},  {128, 256, 920, 3800},  {192, 256, 1110, 4000},
-                               {224, 256, 1220, 5000}, {256, 256, 1340, 6000}};
+constexpr TileCost kTiles[] = {{32, 64, 180, 345, 2300},    {64, 64, 240, 520, 2300},  {64, 128, 340, 1015, 3000},
+                               {128, 128, 560, 1905, 3500}, {128, 256, 920, 0, 3800},  {192, 256, 1110, 0, 4000},
+                               {224, 256, 1220, 0, 5000},   {256, 256, 1340, 0, 6000}};
 
 // The shape with the smallest estimated time for a product of `rows` weight rows.
 template <typename E> Tile pick_tile(double M, double rows, double slabs) {
@@ -214,8 +215,7 @@ template <typename E> Tile pick_tile(double M, double rows, double slabs) {
     for (int i = T32x64; i <= (sizeof(E) == 2 ? T256x256 : T128x128); ++i) {
         const TileCost &t = kTiles[i];
         const double rounds = std::ceil(std::ceil(M / t.bm) * std::ceil(rows / t.bn) / 256.0);
-        const double slab = sizeof(E) == 2 ? t.slab : std::max(t.slab, 2400.0 * t.bm * t.bn / 16384.0);
-        const double c = rounds * (slabs * slab + t.once);
+        const double c = rounds * (slabs * (sizeof(E) == 2 ? t.slab : t.slab_f32) + t.once);
         if (c < cost) {
             cost = c;
             best = (Tile)i;
@@ -235,11 +235,15 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
         if (tile == T192x256) return launch_big<O, GATED, 6>(a, st);
         if (tile == T128x256) return launch_tile<E, O, 128, GATED ? 128 : 256, 2, 4, 3, 1, GATED>(a, st);
     }
+    // Float32 is bound by its MFMAs (eight a step where bf16 has one): fewer stages
+    // and two workgroups a CU, one's products over the other's waits (12608 x 768 ->
+    // 3000: 561 us with one, 475 with two; the library's product 484).
+    constexpr bool F = sizeof(E) == 4;
     switch (tile) {
     case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, 5, 2, GATED>(a, st);
-    case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, 4, 2, GATED>(a, st);
-    case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 5, 1, GATED>(a, st);
-    default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 4, 1, GATED>(a, st);
+    case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, F ? 2 : 4, 2, GATED>(a, st);
+    case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, F ? 3 : 5, 1, GATED>(a, st);
+    default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, F ? 2 : 4, 1, GATED>(a, st);
     }
 }
 

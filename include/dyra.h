@@ -387,10 +387,13 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
  * Y         device, dtype, [T][c]; may be the residual, and X too.
  * workspace device, >= dyra_moe_workspace_bytes(T, topk, f, dtype) bytes,
  *           contents on entry ignored; calls that overlap in time need separate
- *           ones.  It holds the experts' inner activations in dtype.
+ *           ones.  It holds the experts' inner activations in dtype.  With
+ *           8192 bytes more for each token, layers of c < 2048 may share the
+ *           second product's f among workgroups (faster; the sums run in another
+ *           order).
  * T * topk <= 1024, topk <= 64, experts <= 1024 (DYRA_ERR_SHAPE otherwise: more
- * tokens go in several calls).  The sums of a token run in the order of its
- * places, so equal calls give equal bits.
+ * tokens go in several calls).  The order of all sums follows from the arguments
+ * alone, so equal calls give equal bits.
  */
 dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f, const void *Wg,
                      const void *Wu, const void *Wd, int32_t experts, const int32_t *ids, const float *weights,

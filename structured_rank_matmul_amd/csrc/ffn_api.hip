@@ -155,12 +155,14 @@ dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f
     if (overlaps(Y, ldy, T, nullptr, Wg, Wu, residual, ldr) || Y == Wd || workspace == Y || workspace == X ||
         (workspace == residual))
         return DYRA_ERR_ARG;
+    const size_t inner = dyra_moe_workspace_bytes(T, topk, f, dtype);
+    float *const parts = workspace_bytes >= inner + (size_t)T * dyra::kMoePartBytes ? (float *)((char *)workspace + inner) : nullptr;
     hipStream_t st = (hipStream_t)stream;
     auto go = [&](auto e) {
         typedef decltype(e) E;
         const dyra::MoeArgs<E> a{(const E *)X, ldx, (const E *)Wg, (const E *)Wu, (const E *)Wd, ids, weights, c, f,
                                  (int)T, topk, experts, (int)act, (const E *)residual, residual ? ldr : 0, (E *)Y, ldy,
-                                 (E *)workspace};
+                                 (E *)workspace, parts};
         return hip_status(dyra::launch_moe<E>(a, st));
     };
     return dtype == DYRA_BF16 ? go(bf16{}) : go(float{});

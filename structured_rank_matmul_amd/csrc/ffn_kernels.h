@@ -55,10 +55,13 @@ template <typename E> struct MoeArgs {
     E *Y;
     int64_t ldy;
     E *H;              // [T k][f], workspace
+    float *parts;      // kMoePartBytes a token, workspace, or null
 };
 // Pairs (token, place) that one call takes.
 constexpr int kMoeMaxPairs = 1024;
 constexpr int kMoeMaxExperts = 1024;
+// Of split sums, a token: at most 256 workgroups of 8 features in float32.
+constexpr int kMoePartBytes = 256 * 8 * 4;
 template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st);
 
 }  // namespace dyra

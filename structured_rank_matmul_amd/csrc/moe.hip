@@ -345,8 +345,12 @@ template <int ROWS, int SLOT> struct DownLds {
 };
 // Slots hold SLOT pairs: of 8, the ring holds more weights; of 16, an expert of
 // more than 8 pairs is read once.
+//
+// Where c gives fewer workgroups than CUs, gridDim.z of them share the slabs of
+// the same features, each dealing its part to its wavefronts as above, and leave
+// the tokens' sums in `parts` for moe_join_kernel.
 template <typename E, int ROWS, int SLOT>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk) {
+__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk, float *parts) {
     __shared__ __align__(16) DownLds<ROWS, SLOT> lds;
     float *const P = lds.sums, *const weight = lds.weight;
     auto &L = lds.slots;
@@ -361,20 +365,22 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         const int e = ids[p];
         const bool chosen = e >= 0 && e < a.experts;
         weight[p] = chosen ? a.w[(int64_t)t0 * a.k + p] : 0.f;
-        if (!chosen) {  // adds 0
+        if (!chosen || parts) {  // adds 0, or what this workgroup has of it
 #pragma unroll
             for (int q = 0; q < ROWS; ++q) P[p * ROWS + q] = 0.f;
         }
     }
     // the residual of this thread's first result, ahead of the stream
     float residual = 0.f;
-    if (a.R && tid < tn * ROWS && c0 + tid % ROWS < a.c)
+    if (a.R && !parts && tid < tn * ROWS && c0 + tid % ROWS < a.c)
         residual = to_f32(a.R[(int64_t)(t0 + tid / ROWS) * a.ldr + c0 + tid % ROWS]);
     L.build(ids, places, a.experts, reinterpret_cast<int *>(lds.ring));
     const int row_bytes = (int)(a.f * (int)sizeof(E));
     const int slabs = (row_bytes + 127) / 128;
     const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(L.n) * slabs;
-    auto run_start = [&](int v) { return total * v / kWaves; };
+    const int runs = kWaves * (int)gridDim.z, run0 = kWaves * (int)blockIdx.z;
+    auto run_start = [&](int v) { return total * (run0 + v) / runs; };
+    if (parts) __syncthreads();  // the sums' zeros
     const int64_t r0 = run_start(wave), r1 = run_start(wave + 1);
 
     SlabRows w, x;
@@ -408,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
     for (int p = 0; p < ring.DEPTH; ++p) ahead();
 
     int slot = (int)(r0 / slabs), slab = (int)(r0 % slabs);
-    bool begun = slab != 0;  // by the run before
+    bool begun = slab != 0 && wave != 0;  // by the run before, of this workgroup
     f32x4 acc = {};
 #pragma unroll 1
     for (int64_t r = r0; r < r1; ++r) {
@@ -446,10 +452,28 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         if (c0 + q >= a.c) continue;
         float sum = 0.f;
         for (int j = 0; j < a.k; ++j) sum += weight[t * a.k + j] * P[(t * a.k + j) * ROWS + q];
+        if (parts) {
+            parts[((int64_t)blockIdx.z * a.T + tok) * a.c + c0 + q] = sum;
+            continue;
+        }
         if (u < kThreads) sum += residual;
         else if (a.R) sum += to_f32(a.R[tok * a.ldr + c0 + q]);
         a.Y[tok * a.ldy + c0 + q] = to_elem<E>(sum);
     }
+}
+
+// Y = R + the parts of every token, in their order; four columns a thread.
+template <typename E>
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs<E> a, const float *__restrict__ parts, int splits) {
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = a.c / 4;
+    if (u >= a.T * quads) return;
+    const int64_t t = u / quads, c = 4 * (u - t * quads);
+    f32x4 sum = {};
+#pragma unroll 4
+    for (int z = 0; z < splits; ++z) sum += *reinterpret_cast<const f32x4 *>(parts + (z * (int64_t)a.T + t) * a.c + c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        a.Y[t * a.ldy + c + q] = to_elem<E>(sum[q] + (a.R ? to_f32(a.R[t * a.ldr + c + q]) : 0.f));
 }
 
 template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipStream_t st) {
@@ -459,9 +483,19 @@ template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipSt
 }
 template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
     const int chunk = std::min(a.T, kDownPairs<ROWS> / a.k);
-    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>),
-                       dim3((unsigned)((a.c + ROWS - 1) / ROWS), (unsigned)((a.T + chunk - 1) / chunk)), dim3(kThreads),
-                       0, st, a, chunk);
+    const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
+    // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
+    // there are CUs for, down to 150 KB each, where that saves more than the join
+    // costs (3 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 -> SPLITUS us.
+    const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + SLOT);
+    const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
+    const bool split = splits > 1 && a.parts && (double)bytes * (1 - 1.0 / (double)splits) > 200e3;
+    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
+                       dim3(kThreads), 0, st, a, chunk, split ? a.parts : nullptr);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split) return e;
+    hipLaunchKernelGGL((moe_join_kernel<E>), dim3((unsigned)((a.T * (a.c / 4) + 255) / 256)), dim3(256), 0, st, a, a.parts,
+                       (int)splits);
     return hipGetLastError();
 }
 

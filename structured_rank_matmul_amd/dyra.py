@@ -585,7 +585,7 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     else:
         ldy = _matrix(Y, "Y", dev, T, c, t)
     if workspace is None:
-        workspace = _new((max(T * topk * f, 16),), t, X, stream)
+        workspace = _new((T * topk * f + 16 + 8192 * T // X.element_size(),), t, X, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on GPU {dev}")
     _run((_lib or load()).dyra_moe, "dyra_moe", dev, stream, X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk,

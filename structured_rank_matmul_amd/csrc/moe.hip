@@ -486,10 +486,12 @@ template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E
     const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
     // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
     // there are CUs for, down to 150 KB each, where that saves more than the join
-    // costs (3 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 -> SPLITUS us.
+    // costs (3 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 -> 29 us
+    // and 5.
     const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + SLOT);
     const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
-    const bool split = splits > 1 && a.parts && (double)bytes * (1 - 1.0 / (double)splits) > 200e3;
+    const bool split = splits > 1 && a.parts && splits * a.c * 4 <= kMoePartBytes &&
+                       (double)bytes * (1 - 1.0 / (double)splits) > 200e3;
     hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
                        dim3(kThreads), 0, st, a, chunk, split ? a.parts : nullptr);
     hipError_t e = hipGetLastError();
@@ -524,11 +526,12 @@ template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st)
                          : slabs <= 8 ? launch_up<E, 8>(a, st)
                                       : launch_up<E, 12>(a, st);
     if (e != hipSuccess) return e;
-    // 8 rows a workgroup where 16 would leave CUs without one or read the
-    // weights for a second chunk of tokens; slots of 8 where experts have 4 pairs
-    // on average
+    // 8 rows a workgroup while that gives no more workgroups than CUs (each takes
+    // one), or where 16 would read the weights for a second chunk of tokens; else
+    // 16: 8 tokens, 32 experts, 4 places, 2880 x 1024 72 us against 86.  Slots of 8
+    // where experts have 4 pairs on average
     const bool few = a.T <= 8 || pairs <= 6 * a.experts;
-    if (a.c <= 16 * 255 || pairs > kDownPairs<16>) return few ? launch_down<E, 8, 8>(a, st) : launch_down<E, 8, 16>(a, st);
+    if (a.c <= 8 * 256 || pairs > kDownPairs<16>) return few ? launch_down<E, 8, 8>(a, st) : launch_down<E, 8, 16>(a, st);
     return few ? launch_down<E, 16, 8>(a, st) : launch_down<E, 16, 16>(a, st);
 }
 

@@ -221,3 +221,27 @@ def test_expert_layer_over_its_input():
     y = x.cuda()
     dyra.dyra_moe(y, *(v.cuda() for v in (*w3, ids, w)), residual=y, Y=y)
     close(y, *moe_ref(x, *w3, ids, w, "silu", x))
+
+
+# narrow layers: the second product shared among workgroups, runs that begin and end inside slots, experts without pairs
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E,k,c,f", [(57, 9, 4, 360, 5432), (1, 3, 2, 8, 70000), (5, 40, 4, 72, 3000), (15, 20, 1, 456, 2056),
+                                       (300, 6, 3, 16, 1032), (2, 6, 2, 1000, 9008), (64, 8, 8, 264, 1304)])
+def test_moe_narrow(T, E, k, c, f, dtype):
+    import torch
+    t = types()[dtype]
+    x, r, w3 = rand((T, c), 71, t), rand((T, c), 72, t), experts(E, c, f, 73, t)
+    g = torch.Generator().manual_seed(76)
+    ids = torch.randint(0, E + 1, (T, k), generator=g, dtype=torch.int32)
+    ids[:, 0][ids[:, 0] == 2] = -1
+    w = torch.rand(T, k, generator=g)
+    dev = [v.cuda() for v in (x, *w3, ids, w)]
+    ref = on_gpu(moe_ref_grouped, x, *w3, ids, w, "gelu", r)
+    y = dyra.dyra_moe(*dev, act="gelu", residual=r.cuda())
+    close(y, *ref)
+    assert torch.equal(y, dyra.dyra_moe(*dev, act="gelu", residual=r.cuda()))
+    small = torch.empty(dyra.dyra_moe_workspace_bytes(T, k, f, t), dtype=torch.uint8, device="cuda")   # not shared
+    close(dyra.dyra_moe(*dev, act="gelu", residual=r.cuda(), workspace=small), *ref)
+    wide = torch.full((T + 1, c + 3), 7.0, dtype=t, device="cuda")
+    dyra.dyra_moe(*dev, act="gelu", residual=r.cuda(), Y=wide[:T, 1:1 + c])
+    assert torch.equal(wide[:T, 1:1 + c], y) and (wide[T] == 7).all() and (wide[:, 0] == 7).all() and (wide[:, 1 + c:] == 7).all()

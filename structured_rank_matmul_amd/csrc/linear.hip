@@ -21,6 +21,13 @@
 // (block q, row i holds feature 8 (i / 4) + 4 q + i % 4 of the pair's 32): the
 // epilogue stores 16 bytes per lane straight from registers, 64 bytes of a row
 // per instruction, with no pass through LDS.
+//
+// Small tiles are bound by reading their fragments from LDS (a 64 x 128 slab: 64
+// KB by eight wavefronts of 32 x 32).  So the wavefronts form KS groups that take
+// the 32-deep steps in turn on larger parts of the tile (64 x 64: 32 KB), and add
+// their sums through LDS at the end: bf16 slabs of 32 x 64, 64 x 64, 64 x 128, 128 x
+// 128 and 128 x 256 tiles take 149, 179, 291, 498 and 830 ns where one group of
+// smaller parts took 163, 194, 349, 549 and 913.
 #include "linear_big.h"
 
 #include <algorithm>
@@ -30,8 +37,8 @@ namespace dyra {
 
 namespace {
 
-template <typename E, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED> struct TileShape {
-    static constexpr int NW = WM * WN;
+template <typename E, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED> struct TileShape {
+    static constexpr int NW = WM * WN * KS;
     static constexpr int BN = GATED ? 2 * BF : BF;   // rows of the weight panel
     static constexpr int TM = BM / WM / 16;          // token blocks of a wavefront
     static constexpr int TF = BF / WN / 16;          // feature blocks of a wavefront (per product)
@@ -40,17 +47,20 @@ template <typename E, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED
     static constexpr int SLAB = (BM + BN) * 128, STAGE = SL * SLAB;
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0 && BF / 8 % NW == 0, "whole copies per panel");
     static constexpr int PER_CU = NS * STAGE <= 80 * 1024 ? 2 : 1;  // workgroups
+    static constexpr int STEPS = SL * 4 / (int)sizeof(E);  // 32-deep steps of a stage
+    static_assert(STEPS % KS == 0 && TM % KS == 0, "whole steps and token blocks for each K group");
+    static_assert((KS - 1) * (TM / KS) * TN * 1024 * NW <= NS * STAGE, "room for the K groups' sums");
     static_assert(TF % 2 == 0 && TM >= 1 && BF % 32 == 0 && NS * STAGE <= 160 * 1024, "tile shape");
 };
 
-template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL, GATED>::PER_CU * WM * WN / 4)) void linear_tile_kernel(
-    LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
-    using S = TileShape<E, BM, BF, WM, WN, NS, SL, GATED>;
+template <typename E, typename O, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN * KS, (TileShape<E, BM, BF, WM, WN, KS, NS, SL, GATED>::PER_CU * WM * WN * KS / 4)) void
+linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
+    using S = TileShape<E, BM, BF, WM, WN, KS, NS, SL, GATED>;
     __shared__ __align__(16) char smem[NS * S::STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+    const int kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;  // K group, place in the tile
     const int i16 = lane & 15, g = lane >> 4;
     // workgroup ids are dealt round-robin over the 8 XCDs; each XCD walks a
     // contiguous band of tiles, down the tokens first, so tiles that share
@@ -125,10 +135,10 @@ __global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL,
                 return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         };
-        constexpr int STEPS = 4 / (int)sizeof(E);  // 32-deep steps of a slab
+        constexpr int PER_SLAB = 4 / (int)sizeof(E);  // steps of a slab
 #pragma unroll
-        for (int hh = 0; hh < SL * STEPS; ++hh) {
-            const int slab = hh / STEPS * S::SLAB, h = hh % STEPS;
+        for (int step = 0; step < S::STEPS / KS; ++step) {
+            const int hh = KS * step + kg, slab = hh / PER_SLAB * S::SLAB, h = hh % PER_SLAB;
             F fw[S::TN], fx[S::TM];
 #pragma unroll
             for (int j = 0; j < S::TN; ++j) {
@@ -144,6 +154,40 @@ __global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL,
         }
     }
     wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
+    // ---- the K groups' sums: group q finishes token blocks q, q + KS, ..
+    constexpr int OWN = S::TM / KS;
+    f32x4 sum[OWN][S::TN];
+    if constexpr (KS == 1) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) sum[i][j] = acc[i][j];
+    } else {
+        barrier_only();  // every wavefront is done with the stages
+        // [tile place][giving group, the owner left out][owner][block][lane]
+        auto place = [&](int from, int to) {
+            const int slot = ((wm * WN + wn) * (KS - 1) + (from - (from > to))) * KS + to;
+            return smem + (slot * OWN * S::TN * 64 + lane) * 16;
+        };
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            if (i % KS == kg) {
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j) sum[i / KS][j] = acc[i][j];
+            } else {
+                char *const p = place(kg, i % KS);
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j) *reinterpret_cast<f32x4 *>(p + (i / KS * S::TN + j) * 1024) = acc[i][j];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 1; o < KS; ++o) {
+            const char *const p = place((kg + o) % KS, kg);
+#pragma unroll
+            for (int q = 0; q < OWN * S::TN; ++q) sum[q / S::TN][q % S::TN] += *reinterpret_cast<const f32x4 *>(p + q * 1024);
+        }
+    }
     // ---- epilogue: 8 consecutive features of one token per pair of blocks
 #pragma unroll
     for (int p = 0; p < S::TF / 2; ++p) {
@@ -154,23 +198,23 @@ __global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL,
         if (a.b0) load_row(a.b0 + c, b0, have);
         if (GATED && a.b1) load_row(a.b1 + c, b1, have);
         const bool ahead = !GATED && a.R && have >= 8;
-        Residual8<O> r[S::TM];
+        Residual8<O> r[OWN];
         if (ahead) {
 #pragma unroll
-            for (int i = 0; i < S::TM; ++i)
-                r[i].request(a.R + std::min<int64_t>(row0 + (wm * S::TM + i) * 16 + i16, a.M - 1) * a.ldr + c);
+            for (int i = 0; i < OWN; ++i)
+                r[i].request(a.R + std::min<int64_t>(row0 + (wm * S::TM + KS * i + kg) * 16 + i16, a.M - 1) * a.ldr + c);
         }
 #pragma unroll
-        for (int i = 0; i < S::TM; ++i) {
-            const int64_t t = row0 + (wm * S::TM + i) * 16 + i16;
+        for (int i = 0; i < OWN; ++i) {
+            const int64_t t = row0 + (wm * S::TM + KS * i + kg) * 16 + i16;
             if (t >= a.M) continue;
             float v[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = acc[i][2 * p + (q >> 2)][q & 3] + b0[q];
+            for (int q = 0; q < 8; ++q) v[q] = sum[i][2 * p + (q >> 2)][q & 3] + b0[q];
             activate<sizeof(O) == 4>(v, a.act);
             if constexpr (GATED) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] *= acc[i][S::TF + 2 * p + (q >> 2)][q & 3] + b1[q];
+                for (int q = 0; q < 8; ++q) v[q] *= sum[i][S::TF + 2 * p + (q >> 2)][q & 3] + b1[q];
             } else if (ahead) {
                 r[i].add_to(v);
             } else if (a.R) {
@@ -181,14 +225,14 @@ __global__ __launch_bounds__(64 * WM * WN, (TileShape<E, BM, BF, WM, WN, NS, SL,
     }
 }
 
-template <typename E, typename O, int BM, int BF, int WM, int WN, int NS, int SL, bool GATED>
+template <typename E, typename O, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED>
 hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BF - 1) / BF;
     const int64_t ntiles = tiles_m * tiles_n;
     if (ntiles > (int64_t)INT32_MAX - 8) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
-    hipLaunchKernelGGL((linear_tile_kernel<E, O, BM, BF, WM, WN, NS, SL, GATED>), dim3((unsigned)(8 * per_xcd)),
-                       dim3(64 * WM * WN), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd);
+    hipLaunchKernelGGL((linear_tile_kernel<E, O, BM, BF, WM, WN, KS, NS, SL, GATED>), dim3((unsigned)(8 * per_xcd)),
+                       dim3(64 * WM * WN * KS), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd);
     return hipGetLastError();
 }
 
@@ -204,8 +248,8 @@ struct TileCost {
     int bm, bn;
     double slab, slab_f32, once;
 };
-constexpr TileCost kTiles[] = {{32, 64, 180, 345, 2300},    {64, 64, 240, 520, 2300},  {64, 128, 340, 1015, 3000},
-                               {128, 128, 560, 1905, 3500}, {128, 256, 920, 0, 3800},  {192, 256, 1110, 0, 4000},
+constexpr TileCost kTiles[] = {{32, 64, 150, 345, 2500},    {64, 64, 230, 520, 2500},  {64, 128, 305, 1015, 3500},
+                               {128, 128, 550, 1905, 4000}, {128, 256, 870, 0, 5500},  {192, 256, 1110, 0, 4000},
                                {224, 256, 1220, 0, 5000},   {256, 256, 1340, 0, 6000}};
 
 // The shape with the smallest estimated time for a product of `rows` weight rows.
@@ -233,17 +277,23 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
         if (tile == T256x256) return launch_big<O, GATED, 8>(a, st);
         if (tile == T224x256) return launch_big<O, GATED, 7>(a, st);
         if (tile == T192x256) return launch_big<O, GATED, 6>(a, st);
-        if (tile == T128x256) return launch_tile<E, O, 128, GATED ? 128 : 256, 2, 4, 3, 1, GATED>(a, st);
-    }
-    // Float32 is bound by its MFMAs (eight a step where bf16 has one): fewer stages
-    // and two workgroups a CU, one's products over the other's waits (12608 x 768 ->
-    // 3000: 561 us with one, 475 with two; the library's product 484).
-    constexpr bool F = sizeof(E) == 4;
-    switch (tile) {
-    case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, 5, 2, GATED>(a, st);
-    case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, F ? 2 : 4, 2, GATED>(a, st);
-    case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, F ? 3 : 5, 1, GATED>(a, st);
-    default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, F ? 2 : 4, 1, GATED>(a, st);
+        switch (tile) {
+        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 1, GATED ? 1 : 2, 2, 5, 2, GATED>(a, st);
+        case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 1, GATED ? 1 : 2, 4, 4, 2, GATED>(a, st);
+        case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, 1, 2, 4, 3, 2, GATED>(a, st);
+        case T128x128: return launch_tile<E, O, 128, GATED ? 64 : 128, 2, 2, 2, 4, 1, GATED>(a, st);
+        default: return launch_tile<E, O, 128, GATED ? 128 : 256, 2, 2, 2, 3, 1, GATED>(a, st);
+        }
+    } else {
+        // Float32 is bound by its MFMAs (eight a step where bf16 has one): fewer stages
+        // and two workgroups a CU, one's products over the other's waits (12608 x 768 ->
+        // 3000: 561 us with one, 475 with two; the library's product 484).
+        switch (tile) {
+        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, 1, 5, 2, GATED>(a, st);
+        case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, 1, 2, 2, GATED>(a, st);
+        case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 1, 3, 1, GATED>(a, st);
+        default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 1, 2, 1, GATED>(a, st);
+        }
     }
 }
 

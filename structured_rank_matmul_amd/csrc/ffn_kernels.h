@@ -33,6 +33,8 @@ template <typename E, typename O> struct LinearArgs {
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st);
 // Few tokens: the weights are streamed once.
 template <typename E, typename O, bool GATED> hipError_t launch_skinny(const LinearArgs<E, O> &a, hipStream_t st);
+// Few features (up to 32, gated 16) of many tokens: X is streamed.
+template <typename E, typename O, bool GATED> hipError_t launch_narrow(const LinearArgs<E, O> &a, hipStream_t st);
 
 // Router: the k largest of every row of logits.
 template <typename E>

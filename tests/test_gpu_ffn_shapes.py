@@ -245,3 +245,49 @@ def test_moe_narrow(T, E, k, c, f, dtype):
     wide = torch.full((T + 1, c + 3), 7.0, dtype=t, device="cuda")
     dyra.dyra_moe(*dev, act="gelu", residual=r.cuda(), Y=wide[:T, 1:1 + c])
     assert torch.equal(wide[:T, 1:1 + c], y) and (wide[T] == 7).all() and (wide[:, 0] == 7).all() and (wide[:, 1 + c:] == 7).all()
+
+
+# few features of many tokens: one and two blocks of features, K that fits the registers and past it, ends inside a unit
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("N,c1,c2", [(33, 8, 1), (40, 520, 16), (1000, 2056, 17), (4097, 264, 32), (70, 4104, 5), (257, 6200, 31),
+                                     (50, 12296, 16), (65, 16392, 9), (9000, 72, 6), (100, 1024, 33)])
+def test_few_features(N, c1, c2, dtype, out):
+    import torch
+    t, o = types()[dtype], types()[out]
+    x, w, w2 = rand((N, c1 + 16), 81, t), rand((c2, c1 + 8), 82, t, c1 ** -0.5), rand((c2, c1), 83, t, c1 ** -0.5)
+    b, r = rand((c2,), 84, t), rand((N, c2), 85, o)
+    xd, wd, w2d, bd, rd = (v.cuda() for v in (x, w, w2, b, r))
+    x, w, xs, ws = x[:, 8:8 + c1], w[:, 8:8 + c1], xd[:, 8:8 + c1], wd[:, 8:8 + c1]
+    close(dyra.dyra_linear(xs, ws, out_dtype=o), *on_gpu(linear_ref, x, w, None, "none", None, o))
+    wide = torch.full((N + 1, c2 + 3), 7.0, dtype=o, device="cuda")
+    dyra.dyra_linear(xs, ws, bias=bd, act="gelu", residual=rd, out_dtype=o, Y=wide[:N, 1:1 + c2])
+    close(wide[:N, 1:1 + c2], *on_gpu(linear_ref, x, w, b, "gelu", r, o))
+    assert (wide[N] == 7).all() and (wide[:, 0] == 7).all() and (wide[:, 1 + c2:] == 7).all()
+    if dtype == out:
+        w, ws = w.contiguous(), ws.contiguous()
+        close(dyra.dyra_gated(xs, ws, w2d, bias_g=bd), *on_gpu(gated_ref, x, w, w2, b, None, "silu", t))
+        close(dyra.dyra_gated(xs, w2d, ws, bias_u=bd, act="relu"), *on_gpu(gated_ref, x, w2, w, None, b, "relu", t))
+
+
+def test_few_features_infinities_and_nan_stay_in_their_rows():
+    import torch
+    x, w = rand((400, 72), 86, torch.bfloat16), rand((20, 72), 87, torch.bfloat16)
+    clean = dyra.dyra_linear(x.cuda(), w.cuda(), act="silu")
+    x[1, 5], x[399, 71] = float("inf"), float("nan")
+    y = dyra.dyra_linear(x.cuda(), w.cuda(), act="silu")
+    rows = [i for i in range(400) if i not in (1, 399)]
+    assert torch.equal(y[rows], clean[rows]) and y[399].isnan().all() and not y[1].isfinite().all()
+
+
+# several units a workgroup: tokens in registers, K of every number of slabs they hold, and past it
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,row_bytes,c2", [(5, 1040, 8200), (16, 4112, 8211), (16, 8192, 8200), (7, 16400, 8200), (16, 24576, 8200),
+                                            (16, 24592, 8200), (17, 4096, 4200), (32, 8208, 4200), (31, 12288, 4201), (32, 12304, 4200)])
+def test_few_tokens_several_units(N, row_bytes, c2, dtype):
+    t = types()[dtype]
+    c1 = row_bytes // (2 if dtype == "bf16" else 4)
+    x, w, b, r = rand((N, c1), 91, t), rand((c2, c1), 92, t, c1 ** -0.5), rand((c2,), 93, t), rand((N, c2), 94, t)
+    d = [v.cuda() for v in (x, w, b, r)]
+    close(dyra.dyra_linear(d[0], d[1], bias=d[2], act="gelu", residual=d[3]), *on_gpu(linear_ref, x, w, b, "gelu", r, t))
+    w2 = w.flip(0)
+    close(dyra.dyra_gated(d[0], d[1], w2.cuda(), bias_g=d[2]), *on_gpu(gated_ref, x, w, w2, b, None, "silu", t))

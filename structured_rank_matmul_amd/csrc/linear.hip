@@ -48,8 +48,9 @@ template <typename E, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bo
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0 && BF / 8 % NW == 0, "whole copies per panel");
     static constexpr int PER_CU = NS * STAGE <= 80 * 1024 ? 2 : 1;  // workgroups
     static constexpr int STEPS = SL * 4 / (int)sizeof(E);  // 32-deep steps of a stage
-    static_assert(STEPS % KS == 0 && TM % KS == 0, "whole steps and token blocks for each K group");
-    static_assert((KS - 1) * (TM / KS) * TN * 1024 * NW <= NS * STAGE, "room for the K groups' sums");
+    static constexpr int OWNERS = KS < TM ? KS : TM;  // K groups that finish token blocks
+    static_assert(STEPS % KS == 0 && TM % OWNERS == 0, "whole steps for each K group, token blocks for each owner");
+    static_assert((KS - 1) * TM * TN * 1024 * WM * WN <= NS * STAGE, "room for the K groups' sums");
     static_assert(TF % 2 == 0 && TM >= 1 && BF % 32 == 0 && NS * STAGE <= 160 * 1024, "tile shape");
 };
 
@@ -154,8 +155,8 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
         }
     }
     wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
-    // ---- the K groups' sums: group q finishes token blocks q, q + KS, ..
-    constexpr int OWN = S::TM / KS;
+    // ---- the K groups' sums: group q finishes token blocks q, q + OWNERS, ..
+    constexpr int OWN = S::TM / S::OWNERS;
     f32x4 sum[OWN][S::TN];
     if constexpr (KS == 1) {
 #pragma unroll
@@ -164,29 +165,31 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
             for (int j = 0; j < S::TN; ++j) sum[i][j] = acc[i][j];
     } else {
         barrier_only();  // every wavefront is done with the stages
-        // [tile place][giving group, the owner left out][owner][block][lane]
-        auto place = [&](int from, int to) {
-            const int slot = ((wm * WN + wn) * (KS - 1) + (from - (from > to))) * KS + to;
-            return smem + (slot * OWN * S::TN * 64 + lane) * 16;
+        // [tile place][token block][giving group, the owner left out][weight block][lane]
+        auto place = [&](int block, int giver) {
+            return smem + ((((wm * WN + wn) * S::TM + block) * (KS - 1) + giver) * S::TN * 64 + lane) * 16;
         };
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
-            if (i % KS == kg) {
+            const int owner = i % S::OWNERS;
+            if (owner == kg) {
 #pragma unroll
-                for (int j = 0; j < S::TN; ++j) sum[i / KS][j] = acc[i][j];
+                for (int j = 0; j < S::TN; ++j) sum[i / S::OWNERS][j] = acc[i][j];
             } else {
-                char *const p = place(kg, i % KS);
+                char *const p = place(i, kg - (kg > owner));
 #pragma unroll
-                for (int j = 0; j < S::TN; ++j) *reinterpret_cast<f32x4 *>(p + (i / KS * S::TN + j) * 1024) = acc[i][j];
+                for (int j = 0; j < S::TN; ++j) *reinterpret_cast<f32x4 *>(p + j * 1024) = acc[i][j];
             }
         }
         __syncthreads();
+        if (kg >= S::OWNERS) return;
 #pragma unroll
-        for (int o = 1; o < KS; ++o) {
-            const char *const p = place((kg + o) % KS, kg);
+        for (int i = 0; i < OWN; ++i)
 #pragma unroll
-            for (int q = 0; q < OWN * S::TN; ++q) sum[q / S::TN][q % S::TN] += *reinterpret_cast<const f32x4 *>(p + q * 1024);
-        }
+            for (int o = 0; o < KS - 1; ++o)
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+                    sum[i][j] += *reinterpret_cast<const f32x4 *>(place(kg + S::OWNERS * i, o) + j * 1024);
     }
     // ---- epilogue: 8 consecutive features of one token per pair of blocks
 #pragma unroll
@@ -202,11 +205,11 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
         if (ahead) {
 #pragma unroll
             for (int i = 0; i < OWN; ++i)
-                r[i].request(a.R + std::min<int64_t>(row0 + (wm * S::TM + KS * i + kg) * 16 + i16, a.M - 1) * a.ldr + c);
+                r[i].request(a.R + std::min<int64_t>(row0 + (wm * S::TM + S::OWNERS * i + kg) * 16 + i16, a.M - 1) * a.ldr + c);
         }
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const int64_t t = row0 + (wm * S::TM + KS * i + kg) * 16 + i16;
+            const int64_t t = row0 + (wm * S::TM + S::OWNERS * i + kg) * 16 + i16;
             if (t >= a.M) continue;
             float v[8];
 #pragma unroll
@@ -278,7 +281,7 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
         if (tile == T224x256) return launch_big<O, GATED, 7>(a, st);
         if (tile == T192x256) return launch_big<O, GATED, 6>(a, st);
         switch (tile) {
-        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 1, GATED ? 1 : 2, 2, 5, 2, GATED>(a, st);
+        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 1, GATED ? 1 : 2, GATED ? 4 : 2, 5, 2, GATED>(a, st);
         case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 1, GATED ? 1 : 2, 4, 4, 2, GATED>(a, st);
         case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, 1, 2, 4, 3, 2, GATED>(a, st);
         case T128x128: return launch_tile<E, O, 128, GATED ? 64 : 128, 2, 2, 2, 4, 1, GATED>(a, st);

@@ -1,16 +1,21 @@
 // Router and expert layer for a few tokens.
 //
-// Router: a wavefront per row of logits, its values in registers; k rounds of
-// an argmax over keys that order by (value, lower index first).
+// Router: 16 or 64 lanes per row of logits, its values in registers; k rounds of
+// an argmax over keys that order by (value, lower index first).  Bound by the
+// rounds' lane exchanges: 8 of 128 logits in 16384 rows take 8.3 us (8.5 MB read), 8
+// of 64 in 16 rows 3.1, little more than an empty kernel.
 //
-// Expert layer, two kernels.  moe_up forms H[pair][f] = act(X Wg_e^T) * (X Wu_e^T)
-// for every (token, place) pair; moe_down forms Y = R + sum_j w_j H_j Wd_e^T.
-// Both are bound by reading the weights of the chosen experts once: a workgroup
-// gathers the tokens of an expert and multiplies them together, the weights
-// streamed through per-wavefront rings (skinny.h).  Every workgroup sorts the
-// places by expert itself (a few LDS steps), so that two launches do.  No
+// Expert layer, two kernels (three where c is narrow).  moe_up forms H[pair][f] =
+// act(X Wg_e^T) * (X Wu_e^T) for every (token, place) pair; moe_down forms Y = R +
+// sum_j w_j H_j Wd_e^T.  Both are bound by reading the weights of the chosen experts
+// once: a workgroup gathers the tokens of an expert and multiplies them together,
+// the weights streamed through per-wavefront rings (skinny.h).  Every workgroup
+// sorts the places by expert itself (a few LDS steps), so that two launches do.  No
 // atomics on results: every pair's products have a place of their own in LDS and
-// are added per token in the order of its places.
+// are added per token in the order of its places.  Up and down take 137 and 70 us
+// for 48 tokens with 6 places over 64 experts of 2048 x 1408 (1.08 GB, 5.2 TB/s),
+// 325 and 167 for 16 tokens with 2 over 8 of 4096 x 14336 (2.8 GB, 5.7 TB/s), 17.7
+// and 10.8 for 1 token with 8 over 64 of 2048 x 1024 (101 MB, start-up included).
 #include "lanes.h"
 #include "skinny.h"
 
@@ -486,8 +491,8 @@ template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E
     const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
     // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
     // there are CUs for, down to 150 KB each, where that saves more than the join
-    // costs (3 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 -> 29 us
-    // and 5.
+    // costs (5 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 ->
+    // 29 and 5 us.
     const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + SLOT);
     const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
     const bool split = splits > 1 && a.parts && splits * a.c * 4 <= kMoePartBytes &&

@@ -490,13 +490,13 @@ template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E
     const int chunk = std::min(a.T, kDownPairs<ROWS> / a.k);
     const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
     // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
-    // there are CUs for, down to 150 KB each, where that saves more than the join
-    // costs (5 us): 57 tokens, 9 experts, 4 places, 360 x 5432 98 ->
-    // 29 and 5 us.
+    // there are CUs for, down to 150 KB each, where that saves 8 us: the join takes 5
+    // and a launch more of the host.  57 tokens, 9 experts, 4 places, 360 x 5432: 98 ->
+    // 29 + 5 us; 10 tokens, 17 experts, 8 places, 296 x 1064: 15 -> 11 + 4.
     const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + SLOT);
     const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
     const bool split = splits > 1 && a.parts && splits * a.c * 4 <= kMoePartBytes &&
-                       (double)bytes * (1 - 1.0 / (double)splits) > 200e3;
+                       (double)bytes * (1 - 1.0 / (double)splits) > 400e3;
     hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
                        dim3(kThreads), 0, st, a, chunk, split ? a.parts : nullptr);
     hipError_t e = hipGetLastError();

@@ -403,23 +403,26 @@ def dyra_dense_ref(X, Wt, Y=None, stream=None):
 # are written for few Python operations: one read of each tensor property, the
 # raw stream pointer instead of a Stream object.
 
-_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
-_SCORES = {"softmax": 0, "sigmoid": 1}
-_codes: dict = {}   # torch dtype -> dyra_dtype
+class _Names(dict):
+    """Codes by name; an unknown name is a ValueError."""
+    def __init__(self, what, **codes):
+        super().__init__(codes)
+        self.what = what
+
+    def __missing__(self, name):
+        raise ValueError(f"unknown {self.what} {name!r}; known: {sorted(self)}")
 
 
-def _code_of(dtype) -> int:
-    code = _codes.get(dtype)
-    if code is None:
-        code = _codes[dtype] = _dtype_code(dtype)
-    return code
+class _Codes(dict):
+    """dyra_dtype by torch dtype."""
+    def __missing__(self, dtype):
+        code = self[dtype] = _dtype_code(dtype)
+        return code
 
 
-def _named(table, name, what) -> int:
-    code = table.get(name)
-    if code is None:
-        raise ValueError(f"unknown {what} {name!r}; known: {sorted(table)}")
-    return code
+_ACTS = _Names("activation", none=0, relu=1, gelu=2, gelu_tanh=3, silu=4)
+_SCORES = _Names("score", softmax=0, sigmoid=1)
+_codes = _Codes()
 
 
 def _input(X, name="X"):
@@ -481,26 +484,23 @@ def _new(shape, dtype, X, stream):
 _cuda = None   # torch's current device and current raw stream of a device
 
 
-def _run(fn, what, dev, stream, *args) -> None:
-    """fn(*args, stream) with device `dev` current, so that the stream and the launch agree."""
+def _stream_on(dev, stream):
+    """The raw stream for work on device `dev`; None if that is not the current device, which a launch needs it to be."""
     global _cuda
     if _cuda is None:
         import torch
         _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-    if stream is None:
-        st = _cuda[1](dev)
-    elif stream.device_index != dev:
+    if stream is not None and stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {dev}")
-    else:
-        st = stream.cuda_stream
-    if _cuda[0]() == dev:
-        status = fn(*args, st)
-    else:
-        import torch
-        with torch.cuda.device(dev):
-            status = fn(*args, st)
-    if status != 0:
-        raise DyraError(status, what)
+    if _cuda[0]() != dev:
+        return None
+    return _cuda[1](dev) if stream is None else stream.cuda_stream
+
+
+def _with_device(dev, call, *args, **kw):
+    import torch
+    with torch.cuda.device(dev):
+        return call(*args, **kw)
 
 
 def dyra_linear(X, Wt, bias=None, act: str = "none", residual=None, out_dtype=None, Y=None, stream=None):
@@ -508,6 +508,9 @@ def dyra_linear(X, Wt, bias=None, act: str = "none", residual=None, out_dtype=No
     (X's by default; float32 from bfloat16 operands too).  Rows may be strided; a residual expanded from
     one row is added to every token, and Y may be the residual itself."""
     N, c1, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_linear, X, Wt, bias, act, residual, out_dtype, Y, stream)
     t, c2 = X.dtype, Wt.shape[0]
     out = t if out_dtype is None else out_dtype
     ldw = _matrix(Wt, "Wt", dev, c2, c1, t)
@@ -515,12 +518,15 @@ def dyra_linear(X, Wt, bias=None, act: str = "none", residual=None, out_dtype=No
     r, ldr = None, 0
     if residual is not None:
         r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c2, out, True)
+    code = _ACTS[act]
     if Y is None:
         Y, ldy = _new((N, c2), out, X, stream), c2
     else:
         ldy = _matrix(Y, "Y", dev, N, c2, out)
-    _run((_lib or load()).dyra_linear, "dyra_linear", dev, stream, X.data_ptr(), ldx, Wt.data_ptr(), ldw, N, c1, c2,
-         _code_of(t), b, _named(_ACTS, act, "activation"), r, ldr, _code_of(out), Y.data_ptr(), ldy)
+    status = (_lib or load()).dyra_linear(X.data_ptr(), ldx, Wt.data_ptr(), ldw, N, c1, c2, _codes[t], b, code, r, ldr,
+                                          _codes[out], Y.data_ptr(), ldy, st)
+    if status != 0:
+        raise DyraError(status, "dyra_linear")
     return Y
 
 
@@ -528,18 +534,24 @@ def dyra_gated(X, Wg, Wu, bias_g=None, bias_u=None, act: str = "silu", H=None, s
     """H = act(X Wg + bias_g) * (X Wu + bias_u), the gate and up products of a gated MLP; Wg, Wu [c2, c1]
     with one row stride."""
     N, c1, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_gated, X, Wg, Wu, bias_g, bias_u, act, H, stream)
     t, c2 = X.dtype, Wg.shape[0]
     ldw = _matrix(Wg, "Wg", dev, c2, c1, t)
     if _matrix(Wu, "Wu", dev, c2, c1, t) != ldw:
         raise ValueError("Wg and Wu must have one row stride")
     bg = None if bias_g is None else _whole(bias_g, "bias_g", dev, (c2,), t)
     bu = None if bias_u is None else _whole(bias_u, "bias_u", dev, (c2,), t)
+    code = _ACTS[act]
     if H is None:
         H, ldh = _new((N, c2), t, X, stream), c2
     else:
         ldh = _matrix(H, "H", dev, N, c2, t)
-    _run((_lib or load()).dyra_gated, "dyra_gated", dev, stream, X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N,
-         c1, c2, _code_of(t), bg, bu, _named(_ACTS, act, "activation"), H.data_ptr(), ldh)
+    status = (_lib or load()).dyra_gated(X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, c1, c2, _codes[t], bg, bu,
+                                         code, H.data_ptr(), ldh, st)
+    if status != 0:
+        raise DyraError(status, "dyra_gated")
     return H
 
 
@@ -548,13 +560,18 @@ def dyra_route(logits, topk: int, score: str = "softmax", renormalise: bool = Tr
     Masked (-inf) experts are never chosen; places left over hold -1 and 0."""
     import torch
     T, experts, ld, dev = _input(logits, "logits")
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_route, logits, topk, score, renormalise, scale, stream)
     if not 1 <= topk <= experts:
         raise ValueError(f"topk must be in [1, {experts}]")
+    code, score = _codes[logits.dtype], _SCORES[score]
     ids = _new((T, topk), torch.int32, logits, stream)
     weights = _new((T, topk), torch.float32, logits, stream)
-    _run((_lib or load()).dyra_route, "dyra_route", dev, stream, logits.data_ptr(), ld, T, experts, topk,
-         _code_of(logits.dtype), _named(_SCORES, score, "score"), 1 if renormalise else 0, scale, ids.data_ptr(),
-         weights.data_ptr())
+    status = (_lib or load()).dyra_route(logits.data_ptr(), ld, T, experts, topk, code, score, 1 if renormalise else 0,
+                                         scale, ids.data_ptr(), weights.data_ptr(), st)
+    if status != 0:
+        raise DyraError(status, "dyra_route")
     return ids, weights
 
 
@@ -567,6 +584,9 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     X [T, c], Wg and Wu [experts, f, c], Wd [experts, c, f], ids (int32) and weights (float32) [T, topk]."""
     import torch
     T, c, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_moe, X, Wg, Wu, Wd, ids, weights, act, residual, Y, workspace, stream)
     t = X.dtype
     if Wg.dim() != 3 or ids.dim() != 2:
         raise ValueError("Wg must be [experts, f, c] and ids [T, topk]")
@@ -580,6 +600,7 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     r, ldr = None, 0
     if residual is not None:
         r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, T, c, t, True)
+    code = _ACTS[act]
     if Y is None:
         Y, ldy = _new((T, c), t, X, stream), c
     else:
@@ -588,7 +609,9 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
         workspace = _new((T * topk * f + 16 + 8192 * T // X.element_size(),), t, X, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on GPU {dev}")
-    _run((_lib or load()).dyra_moe, "dyra_moe", dev, stream, X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk,
-         _code_of(t), _named(_ACTS, act, "activation"), r, ldr, Y.data_ptr(), ldy, workspace.data_ptr(),
-         workspace.numel() * workspace.element_size())
+    status = (_lib or load()).dyra_moe(X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk, _codes[t], code, r, ldr,
+                                       Y.data_ptr(), ldy, workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), st)
+    if status != 0:
+        raise DyraError(status, "dyra_moe")
     return Y

@@ -292,7 +292,7 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
         // and two workgroups a CU, one's products over the other's waits (12608 x 768 ->
         // 3000: 561 us with one, 475 with two; the library's product 484).
         switch (tile) {
-        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, 1, 5, 2, GATED>(a, st);
+        case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 2, GATED ? 1 : 2, GATED ? 2 : 1, 5, 2, GATED>(a, st);
         case T64x64: return launch_tile<E, O, 64, GATED ? 32 : 64, 4, GATED ? 1 : 2, 1, 2, 2, GATED>(a, st);
         case T64x128: return launch_tile<E, O, 64, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 1, 3, 1, GATED>(a, st);
         default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 1, 2, 1, GATED>(a, st);

@@ -291,3 +291,43 @@ def test_few_tokens_several_units(N, row_bytes, c2, dtype):
     close(dyra.dyra_linear(d[0], d[1], bias=d[2], act="gelu", residual=d[3]), *on_gpu(linear_ref, x, w, b, "gelu", r, t))
     w2 = w.flip(0)
     close(dyra.dyra_gated(d[0], d[1], w2.cuda(), bias_g=d[2]), *on_gpu(gated_ref, x, w, w2, b, None, "silu", t))
+
+
+def test_narrow_layers_captured_and_on_two_streams():
+    """A small router and a narrow expert layer (f shared among workgroups): two graphs replayed in turn, then two streams."""
+    import torch
+    T, E, k, c, f = 40, 12, 2, 264, 6000
+    p = [v.cuda() for v in (rand((E, c), 95, torch.bfloat16, c ** -0.5), *experts(E, c, f, 96, torch.bfloat16))]
+
+    def layer(x, stream=None):
+        logits = dyra.dyra_linear(x, p[0], out_dtype=torch.float32, stream=stream)
+        ids, w = dyra.dyra_route(logits, k, stream=stream)
+        return logits, ids, w, dyra.dyra_moe(x, *p[1:], ids, w, residual=x, stream=stream)
+
+    static = [rand((T, c), 101 + i, torch.bfloat16).cuda() for i in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for x in static:
+            layer(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for x in static:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer(x))
+        graphs.append(g)
+    for i in range(4):
+        for q in range(2):
+            static[q].copy_(rand((T, c), 110 + 2 * i + q, torch.bfloat16))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        eager = [layer(x) for x in static]
+        assert all(torch.equal(u, v) for o, e in zip(outs, eager) for u, v in zip(o, e)), f"replay {i}"
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(layer(static[q], streams[q]), eager[q]) for _ in range(3) for q in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for g, r in got for u, v in zip(g, r))

@@ -390,7 +390,11 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
  *           ones.  It holds the experts' inner activations in dtype.  With
  *           8192 bytes more for each token, layers of c < 2048 may share the
  *           second product's f among workgroups (faster; the sums run in another
- *           order).
+ *           order).  With T * topk * f * 2 bytes more beyond those, the inner
+ *           activations of bfloat16 layers keep 16 bits of mantissa between the
+ *           products, in two parts, rather than 8: an output is then rounded once
+ *           (1 to 20 % slower; an infinite weight of Wd may then give NaN where one
+ *           part of an activation is 0 or of the other sign).
  * T * topk <= 1024, topk <= 64, experts <= 1024 (DYRA_ERR_SHAPE otherwise: more
  * tokens go in several calls).  The order of all sums follows from the arguments
  * alone, so equal calls give equal bits.

@@ -167,13 +167,17 @@ dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f
         (workspace == residual))
         return DYRA_ERR_ARG;
     const size_t inner = dyra_moe_workspace_bytes(T, topk, f, dtype);
-    float *const parts = workspace_bytes >= inner + (size_t)T * dyra::kMoePartBytes ? (float *)((char *)workspace + inner) : nullptr;
+    // what is there beyond the inner activations: room for split sums, then for what
+    // the activations' rounding leaves out
+    const size_t split = (size_t)T * dyra::kMoePartBytes;
+    const bool rest = dtype == DYRA_BF16 && workspace_bytes >= 2 * inner + split;
+    float *const parts = workspace_bytes >= inner + split ? (float *)((char *)workspace + (rest ? 2 : 1) * inner) : nullptr;
     hipStream_t st = (hipStream_t)stream;
     auto go = [&](auto e) {
         typedef decltype(e) E;
         const dyra::MoeArgs<E> a{(const E *)X, ldx, (const E *)Wg, (const E *)Wu, (const E *)Wd, ids, weights, c, f,
                                  (int)T, topk, experts, (int)act, (const E *)residual, residual ? ldr : 0, (E *)Y, ldy,
-                                 (E *)workspace, parts};
+                                 (E *)workspace, rest, parts};
         return hip_status(dyra::launch_moe<E>(a, st));
     };
     return dtype == DYRA_BF16 ? go(bf16{}) : go(float{});

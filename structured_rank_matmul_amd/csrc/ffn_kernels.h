@@ -56,7 +56,8 @@ template <typename E> struct MoeArgs {
     int64_t ldr;
     E *Y;
     int64_t ldy;
-    E *H;              // [T k][f], workspace
+    E *H;              // [T k][f], workspace; with `rest` [T k][f / 8][2][8]
+    bool rest;         // of every 8 features what their rounding left out follows (bf16)
     float *parts;      // kMoePartBytes a token, workspace, or null
 };
 // Pairs (token, place) that one call takes.

@@ -12,10 +12,19 @@
 // the weights streamed through per-wavefront rings (skinny.h).  Every workgroup
 // sorts the places by expert itself (a few LDS steps), so that two launches do.  No
 // atomics on results: every pair's products have a place of their own in LDS and
-// are added per token in the order of its places.  Up and down take 137 and 70 us
-// for 48 tokens with 6 places over 64 experts of 2048 x 1408 (1.08 GB, 5.2 TB/s),
-// 325 and 167 for 16 tokens with 2 over 8 of 4096 x 14336 (2.8 GB, 5.7 TB/s), 17.7
-// and 10.8 for 1 token with 8 over 64 of 2048 x 1024 (101 MB, start-up included).
+// are added per token in the order of its places.  Up and down take 141 and 81 us
+// for 48 tokens with 6 places over 64 experts of 2048 x 1408 (1.08 GB, 4.9 TB/s),
+// 318 and 168 for 16 tokens with 2 over 8 of 4096 x 14336 (2.8 GB, 5.7 TB/s), 17.8
+// and 11.8 for 1 token with 8 over 64 of 2048 x 1024 (101 MB, start-up included).
+//
+// H between the two is a bf16 operand of the second product.  Rounded to it once,
+// it alone puts 1e-3 of a result's size into every result, where the last rounding
+// puts 1.66e-3 (error against float64, 16 tokens with 2 places over 8 experts of
+// 4096 x 14336: 2.00e-3 against 1.66e-3).  So H keeps what the rounding left out as
+// a second bf16 (together to 2^-16 of it), and the second product is taken of both
+// parts: twice the ring bytes of the pairs, 0.5, 11 and 7 us in the cases above, 20
+// of 88 at 512 tokens with 2 places over 8 experts of 1024 x 2816.  A caller whose
+// workspace has no room for the second part has H rounded once.
 #include "lanes.h"
 #include "skinny.h"
 
@@ -321,7 +330,24 @@ template <typename E> struct UpPosition {
         const float *block = sums + (at >> 4) * kWaves * kBlockSums;
         float y[1] = {joined(block, at & 15, q)};
         activate<sizeof(E) == 4>(y, a->act);
-        a->H[(int64_t)L->list[L->first[slot] + at] * a->f + c] = to_elem<E>(y[0] * joined(block, at & 15, 8 + q));
+        const float h = y[0] * joined(block, at & 15, 8 + q);
+        const int64_t pair = L->list[L->first[slot] + at];
+        if constexpr (sizeof(E) == 2) {
+            if (a->rest) {
+                // the eight lanes of a pair hold its eight features: each stores one word of
+                // the 32 bytes (two stores of half words: 8 us more at 48 tokens over 64
+                // experts, as the ring waits for stores too).  Of an infinity nothing is left.
+                const E high = to_elem<E>(h);
+                const E low = to_elem<E>(fabsf(to_f32(high)) < INFINITY ? h - to_f32(high) : 0.f);
+                const uint32_t both = __builtin_bit_cast(uint16_t, high) | (uint32_t)__builtin_bit_cast(uint16_t, low) << 16;
+                const int from = (threadIdx.x & 56) + 2 * (q & 3);
+                const uint32_t even = __shfl(both, from), odd = __shfl(both, from + 1);
+                reinterpret_cast<uint32_t *>(a->H)[pair * a->f + c] =
+                    q < 4 ? (even & 0xffff) | odd << 16 : even >> 16 | (odd & 0xffff0000);
+                return;
+            }
+        }
+        a->H[pair * a->f + c] = to_elem<E>(h);
     }
 };
 
@@ -349,12 +375,15 @@ template <int ROWS, int SLOT> struct DownLds {
     Slots<kDownPairs<ROWS>, SLOT> slots;
 };
 // Slots hold SLOT pairs: of 8, the ring holds more weights; of 16, an expert of
-// more than 8 pairs is read once.
+// more than 8 pairs is read once.  REST: H has two parts, which are rows 2 i and
+// 2 i + 1 of the pairs' slabs, so that a copy reads whole lines; a pair's sum is
+// that of two neighbouring lanes (16 tokens over 8 experts of 4096 x 14336, both
+// kernels: 479 us; as rows i and 8 + i of separate buffers 486).
 //
 // Where c gives fewer workgroups than CUs, gridDim.z of them share the slabs of
 // the same features, each dealing its part to its wavefronts as above, and leave
 // the tokens' sums in `parts` for moe_join_kernel.
-template <typename E, int ROWS, int SLOT>
+template <typename E, int ROWS, int SLOT, bool REST>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int chunk, float *parts) {
     __shared__ __align__(16) DownLds<ROWS, SLOT> lds;
     float *const P = lds.sums, *const weight = lds.weight;
@@ -388,11 +417,12 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
     if (parts) __syncthreads();  // the sums' zeros
     const int64_t r0 = run_start(wave), r1 = run_start(wave + 1);
 
-    SlabRows w, x;
-    SlabRing<E, ROWS, SLOT> ring{lds.ring + wave * kRingBytes};
+    SlabRows w, x, x2;
+    SlabRing<E, ROWS, REST ? 2 * SLOT : SLOT> ring{lds.ring + wave * kRingBytes};
     int64_t in_left = r1 - r0;
     int in_slot = (int)(r0 / slabs), in_slab = (int)(r0 % slabs);
-    x.buf[0] = x.buf[1] = panel(a.H + (int64_t)t0 * a.k * a.f);
+    constexpr int WIDE = REST ? 2 : 1;  // H's row, in rows of Wd
+    x.buf[0] = x.buf[1] = x2.buf[0] = x2.buf[1] = panel(a.H + (int64_t)t0 * a.k * a.f * WIDE);
     auto aim = [&]() __attribute__((always_inline)) {
         const int e = __builtin_amdgcn_readfirstlane(L.expert[in_slot]);
         w.buf[0] = w.buf[1] = panel(a.Wd + ((int64_t)e * a.c + c0) * a.f);
@@ -401,11 +431,15 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         for (int q = 0; q < 2; ++q) {
             w.off[q] = (uint32_t)min(slab_row(q), last) * (uint32_t)row_bytes + slab_chunk(q);
             // rows past the slot's pairs read nothing
-            x.off[q] = slab_row(q) < n ? (uint32_t)L.list[f0 + slab_row(q)] * (uint32_t)row_bytes + slab_chunk(q) : kOutside;
+            // REST: pairs 8 .. 15 in x2
+            const int i = slab_row(q) / WIDE;
+            const uint32_t in_row = WIDE * slab_chunk(q) + (REST ? 16 * (slab_row(q) & 1) : 0);
+            x.off[q] = i < n ? (uint32_t)L.list[f0 + i] * (uint32_t)(WIDE * row_bytes) + in_row : kOutside;
+            x2.off[q] = i + 8 < n ? (uint32_t)L.list[f0 + i + 8] * (uint32_t)(WIDE * row_bytes) + in_row : kOutside;
         }
     };
     auto ahead = [&]() __attribute__((always_inline)) {
-        ring.issue(w, x, 128u * (uint32_t)in_slab, in_left > 0 ? row_bytes - 128 * in_slab : 0);
+        ring.issue(w, x, x2, 128u * (uint32_t)in_slab, 128u * WIDE * (uint32_t)in_slab, in_left > 0 ? row_bytes - 128 * in_slab : 0);
         --in_left;
         if (++in_slab == slabs) {
             in_slab = 0;
@@ -420,20 +454,34 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
 
     int slot = (int)(r0 / slabs), slab = (int)(r0 % slabs);
     bool begun = slab != 0 && wave != 0;  // by the run before, of this workgroup
-    f32x4 acc = {};
+    f32x4 acc = {}, acc2 = {};
+    // the pair of the slot whose sums this lane holds in the end
+    const int mine = REST ? (i16 >> 1) + (SLOT == 16 ? 8 * (i16 & 1) : 0) : i16;
+    const bool keeps = 4 * g < ROWS && (!REST || SLOT == 16 || i16 % 2 == 0);
 #pragma unroll 1
     for (int64_t r = r0; r < r1; ++r) {
-        SlabFrag<E> fw, fx;
-        ring.take(fw, fx);
+        SlabFrag<E> fw, fx, fx2;
+        ring.take(fw, fx, fx2);
         ahead();
         acc = slab_product(acc, fw, fx);
+        if constexpr (REST && SLOT == 16) acc2 = slab_product(acc2, fw, fx2);
         if (++slab == slabs || r + 1 == r1) {
-            if (4 * g < ROWS) {
-                if (begun) *reinterpret_cast<f32x4 *>(&head[wave][i16 * ROWS + 4 * g]) = acc;
-                else if (i16 < L.count[slot])
-                    *reinterpret_cast<f32x4 *>(&P[L.list[L.first[slot] + i16] * ROWS + 4 * g]) = acc;
+            if constexpr (REST) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    acc[t] += __uint_as_float(lane_xor<1>(__float_as_uint(acc[t])));
+                    if constexpr (SLOT == 16) {
+                        acc2[t] += __uint_as_float(lane_xor<1>(__float_as_uint(acc2[t])));
+                        acc[t] = i16 % 2 == 0 ? acc[t] : acc2[t];
+                    }
+                }
             }
-            acc = f32x4{};
+            if (keeps) {
+                if (begun) *reinterpret_cast<f32x4 *>(&head[wave][mine * ROWS + 4 * g]) = acc;
+                else if (mine < L.count[slot])
+                    *reinterpret_cast<f32x4 *>(&P[L.list[L.first[slot] + mine] * ROWS + 4 * g]) = acc;
+            }
+            acc = acc2 = f32x4{};
             begun = false;
             slab = 0;
             ++slot;
@@ -486,18 +534,18 @@ template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipSt
     hipLaunchKernelGGL((moe_up_kernel<E, SLABS>), dim3((unsigned)std::min<int64_t>(most, 256)), dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
-template <typename E, int ROWS, int SLOT> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
+template <typename E, int ROWS, int SLOT, bool REST> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
     const int chunk = std::min(a.T, kDownPairs<ROWS> / a.k);
     const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
     // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
     // there are CUs for, down to 150 KB each, where that saves 8 us: the join takes 5
     // and a launch more of the host.  57 tokens, 9 experts, 4 places, 360 x 5432: 98 ->
     // 29 + 5 us; 10 tokens, 17 experts, 8 places, 296 x 1064: 15 -> 11 + 4.
-    const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + SLOT);
+    const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + (REST ? 2 : 1) * SLOT);
     const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
     const bool split = splits > 1 && a.parts && splits * a.c * 4 <= kMoePartBytes &&
                        (double)bytes * (1 - 1.0 / (double)splits) > 400e3;
-    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
+    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT, REST>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
                        dim3(kThreads), 0, st, a, chunk, split ? a.parts : nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !split) return e;
@@ -536,8 +584,16 @@ template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st)
     // 16: 8 tokens, 32 experts, 4 places, 2880 x 1024 72 us against 86.  Slots of 8
     // where experts have 4 pairs on average
     const bool few = a.T <= 8 || pairs <= 6 * a.experts;
-    if (a.c <= 8 * 256 || pairs > kDownPairs<16>) return few ? launch_down<E, 8, 8>(a, st) : launch_down<E, 8, 16>(a, st);
-    return few ? launch_down<E, 16, 8>(a, st) : launch_down<E, 16, 16>(a, st);
+    const bool eight = a.c <= 8 * 256 || pairs > kDownPairs<16>;
+    auto go = [&](auto rest) {
+        constexpr bool REST = decltype(rest)::value;
+        if (eight) return few ? launch_down<E, 8, 8, REST>(a, st) : launch_down<E, 8, 16, REST>(a, st);
+        return few ? launch_down<E, 16, 8, REST>(a, st) : launch_down<E, 16, 16, REST>(a, st);
+    };
+    if constexpr (sizeof(E) == 2) {
+        if (a.rest) return go(std::true_type{});
+    }
+    return go(std::false_type{});
 }
 
 template hipError_t launch_route<float>(const float *, int64_t, int64_t, int, int, bool, bool, float, int32_t *, float *,

@@ -84,8 +84,9 @@ constexpr int kRingBytes = 16384;  // of LDS for each wavefront's ring
 // one more after each is taken, past the end of the stream slabs of nothing (no
 // byte left: zeros, no memory is read), so that one wait fits every take.  The
 // copies left over have to land before the workgroup ends.  WROWS rows of
-// weights and XROWS of tokens a slab (16 or 8 each, XROWS also 0; with 8, rows
-// 8 .. 15 of the fragments repeat them).
+// weights and XROWS of tokens a slab (16 or 8 each, XROWS also 0 or 32; with 8, rows
+// 8 .. 15 of the fragments repeat them, with 32 there are two fragments of 16).  The
+// tokens' rows may lie anywhere: their slab is at byte `kx` of them.
 template <typename E, int WROWS, int XROWS> struct SlabRing {
     static constexpr int WBYTES = 128 * WROWS, SLAB = WBYTES + 128 * XROWS;
     static constexpr int DEPTH = kRingBytes / SLAB, COPIES = (WROWS + XROWS) / 8;
@@ -100,10 +101,15 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
     // Copies one slab at byte `k` of the rows; `left` bytes of the rows are left.
     __device__ __forceinline__ void issue(const SlabRows &w, uint32_t k, int left) { issue(w, w, k, left); }
     __device__ __forceinline__ void issue(const SlabRows &w, const SlabRows &x, uint32_t k, int left) {
+        issue(w, x, x, k, k, left);
+    }
+    __device__ __forceinline__ void issue(const SlabRows &w, const SlabRows &x, const SlabRows &x2, uint32_t k, uint32_t kx,
+                                          int left) {
         char *dst = ring + at * SLAB;
-        if (left <= 0) k = 0;  // past a short buffer's end the range check could wrap
+        if (left <= 0) k = kx = 0;  // past a short buffer's end the range check could wrap
         copy<WROWS>(w, k, left, dst);
-        if constexpr (XROWS > 0) copy<XROWS>(x, k, left, dst + WBYTES);
+        if constexpr (XROWS > 0) copy<(XROWS < 16 ? XROWS : 16)>(x, kx, left, dst + WBYTES);
+        if constexpr (XROWS == 32) copy<16>(x2, kx, left, dst + WBYTES + 16 * 128);
         at = at + 1 == DEPTH ? 0 : at + 1;
     }
     // Waits for the oldest slab and reads its fragments; the next issue has to
@@ -113,13 +119,18 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
         take(w, none);
     }
     __device__ __forceinline__ void take(SlabFrag<E> &w, SlabFrag<E> &x) {
+        SlabFrag<E> none;
+        take(w, x, none);
+    }
+    __device__ __forceinline__ void take(SlabFrag<E> &w, SlabFrag<E> &x, SlabFrag<E> &x2) {
         // (stores issued in between only make the wait stricter)
         wait_vmcnt<(DEPTH - 1) * COPIES>();
         // the copies write LDS behind the compiler's back: no read may move above the wait
         asm volatile("" ::: "memory");
         const char *slab = ring + at * SLAB;
         w = slab_read<E, WROWS>(slab);
-        if constexpr (XROWS > 0) x = slab_read<E, XROWS>(slab + WBYTES);
+        if constexpr (XROWS > 0) x = slab_read<E, (XROWS < 16 ? XROWS : 16)>(slab + WBYTES);
+        if constexpr (XROWS == 32) x2 = slab_read<E, 16>(slab + WBYTES + 16 * 128);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the fragments are in registers
         asm volatile("" ::: "memory");
     }

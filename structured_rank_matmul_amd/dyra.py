@@ -581,7 +581,10 @@ def dyra_moe_workspace_bytes(T: int, topk: int, f: int, dtype) -> int:
 
 def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=None, workspace=None, stream=None):
     """Y = residual + sum over a token's places of weight * (act(X Wg_e) * (X Wu_e)) Wd_e, for few tokens:
-    X [T, c], Wg and Wu [experts, f, c], Wd [experts, c, f], ids (int32) and weights (float32) [T, topk]."""
+    X [T, c], Wg and Wu [experts, f, c], Wd [experts, c, f], ids (int32) and weights (float32) [T, topk].
+
+    Without a workspace one of 4 T topk f + 8192 T bytes is allocated, with which bfloat16 inner activations
+    keep what their rounding leaves out; with one of dyra_moe_workspace_bytes they are rounded once."""
     import torch
     T, c, ldx, dev = _input(X)
     st = _stream_on(dev, stream)
@@ -606,7 +609,7 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     else:
         ldy = _matrix(Y, "Y", dev, T, c, t)
     if workspace is None:
-        workspace = _new((T * topk * f + 16 + 8192 * T // X.element_size(),), t, X, stream)
+        workspace = _new((4 * T * topk * f + 8192 * T + 16,), torch.uint8, X, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on GPU {dev}")
     status = (_lib or load()).dyra_moe(X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk, _codes[t], code, r, ldr,

@@ -1,0 +1,81 @@
+"""How near the feed-forward operators come to their definitions where a looser bound would hide it.
+
+Bounds as in test_gpu_ffn, but for what each test says.
+"""
+import pytest
+
+from structured_rank_matmul_amd import dyra
+from test_gpu_ffn import close, experts, gated_ref, half, rand, types, U
+from test_gpu_ffn_shapes import moe_ref_grouped, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ inner activations of the expert layer
+
+def moe_ref_once(x, wg, wu, wd, ids, w, act, r):
+    """The expert layer with its output rounded once: inner activations in two bfloat16 parts.  The first leaves out at
+    most half a step (2^-8 of them), the second half a step of that: 2^-16."""
+    import torch
+    t, f = x.dtype, wg.shape[1]
+    y = r.double().clone()
+    terms, d = y.abs().clone(), torch.zeros_like(y)
+    for e in range(wg.shape[0]):
+        at = (ids == e).nonzero()
+        if not len(at):
+            continue
+        i, p = at[:, 0], w[at[:, 0], at[:, 1]].double()[:, None]
+        h, dh = gated_ref(x[i], wg[e], wu[e], None, None, act, torch.float32)
+        dh = dh + 2.0 ** -16 * (h.abs() + dh)
+        wde = wd[e].double()
+        o, s, m = h @ wde.T, h.abs() @ wde.abs().T, dh @ wde.abs().T
+        y.index_add_(0, i, p * o)
+        terms.index_add_(0, i, p.abs() * o.abs())
+        # twice the terms: both parts are summed
+        d.index_add_(0, i, p.abs() * (m + 2 * (2 * f + 4) * U * (s + m)))
+    d += 2 * (ids.shape[1] + 4) * U * (terms + d)
+    return y, d + half(t) * (y.abs() + d)
+
+
+# 8 and 16 rows of Wd a workgroup, slots of 8 and of 16 pairs; more pairs than a chunk; f shared among workgroups
+@pytest.mark.parametrize("T,E,k,c,f", [(1, 8, 3, 64, 40), (5, 8, 2, 256, 1000), (40, 4, 3, 72, 1032), (6, 4, 2, 2056, 520),
+                                       (40, 3, 2, 2056, 1048), (150, 4, 2, 2064, 520), (57, 9, 4, 360, 5432), (200, 3, 5, 24, 72)])
+def test_expert_layer_rounds_its_output_once(T, E, k, c, f):
+    import torch
+    t = torch.bfloat16
+    x, r, w3 = rand((T, c), 1, t), rand((T, c), 2, t), experts(E, c, f, 3, t)
+    g = torch.Generator().manual_seed(6)
+    ids = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)
+    w = torch.rand(T, k, generator=g)
+    dev, args = [v.cuda() for v in (x, *w3, ids, w)], (x, *w3, ids, w, "silu", r)
+    y = dyra.dyra_moe(*dev, residual=r.cuda())
+    close(y, *on_gpu(moe_ref_once, *args))
+    # workspaces without room for the second parts: the inner activations are rounded once more
+    least = dyra.dyra_moe_workspace_bytes(T, k, f, t)
+    for n in (least, least + 8192 * T, 2 * least + 8192 * T - 1):
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        close(dyra.dyra_moe(*dev, residual=r.cuda(), workspace=ws), *on_gpu(moe_ref_grouped, *args), f"{n} bytes")
+    ws = torch.empty(2 * least + 8192 * T, dtype=torch.uint8, device="cuda")
+    assert torch.equal(y, dyra.dyra_moe(*dev, residual=r.cuda(), workspace=ws))
+
+
+@pytest.mark.parametrize("T", [4, 30])
+def test_infinite_inner_activations_stay_in_their_tokens(T):
+    """An inner activation past bfloat16's range has no rest: its token's row is not finite, no other row changes."""
+    import torch
+    t, E, k, c, f = torch.bfloat16, 2, 1, 64, 48
+    x, w3 = rand((T, c), 7, t), experts(E, c, f, 8, t)
+    ids, w = torch.zeros(T, k, dtype=torch.int32), torch.ones(T, k)
+    dev = [v.cuda() for v in w3]
+    clean = dyra.dyra_moe(x.cuda(), *dev, ids.cuda(), w.cuda(), act="none")
+    x[2] *= 1e30                    # gate and up about 1e30 each: their product overflows float32
+    y = dyra.dyra_moe(x.cuda(), *dev, ids.cuda(), w.cuda(), act="none")
+    rows = [i for i in range(T) if i != 2]
+    assert torch.equal(y[rows], clean[rows]) and not y[2].isfinite().any()
+    x[2] = 0
+    w3[0][0, 5], w3[1][0, 5] = 0, 0  # one feature of 2e38 (1e19 * 2e19), the others 0: finite, and so is the result
+    x[2, 0] = 1.0
+    w3[0][0, :, 0], w3[1][0, :, 0] = 0, 0
+    w3[0][0, 5, 0], w3[1][0, 5, 0] = 1e19, 2e19
+    y = dyra.dyra_moe(x.cuda(), *(v.cuda() for v in w3), ids.cuda(), w.cuda(), act="none")
+    assert y[2].isfinite().all()

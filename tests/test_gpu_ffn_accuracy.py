@@ -79,3 +79,66 @@ def test_infinite_inner_activations_stay_in_their_tokens(T):
     w3[0][0, 5, 0], w3[1][0, 5, 0] = 1e19, 2e19
     y = dyra.dyra_moe(x.cuda(), *(v.cuda() for v in w3), ids.cuda(), w.cuda(), act="none")
     assert y[2].isfinite().all()
+
+
+# ------------------------------------------------------------------ gelu where it is small
+
+def gelu_bound(v, out):
+    """gelu(v) and the bound of a result: half a step of the type, and of the activation's own evaluation, for bfloat16
+    results 2^-12 of it, also no more than 16 u |v|; for float32 erfc's: its argument is right to 2 u, which is
+    2 (v^2 + 1) u of the result, itself and the products 20 u."""
+    import math
+
+    import torch
+    v = v.double()
+    y = 0.5 * v * torch.erfc(-v / math.sqrt(2))
+    own = torch.minimum(2.0 ** -12 * y.abs(), 16 * U * v.abs()) if out == torch.bfloat16 else (2 * (v * v + 1) + 20) * U * y.abs()
+    return y, own + half(out) * (y.abs() + own)
+
+
+# the kernels for few tokens (in registers and through the ring), few features, tiles, and the largest tiles
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("N,c2", [(7, 48), (16, 8200), (300, 8), (300, 70), (4000, 2050)])
+def test_gelu_is_right_where_it_is_small(N, c2, dtype, out):
+    """Values from -12.75 on come through the product unchanged; gelu(-5) is -1.4e-6, gelu(-12.75) -2e-36."""
+    import torch
+    t, o = types()[dtype], types()[out]
+    v = torch.linspace(-12.75, 6, N).to(t)
+    v[:4] = torch.tensor([-3.5, -4.5, -5.0, -5.5])
+    x, w, zero = torch.zeros(N, 8, dtype=t), torch.zeros(c2, 8, dtype=t), torch.zeros(c2, 8, dtype=t)
+    x[:, 2], w[:, 2] = v, 1
+    y, bound = gelu_bound(v, o)
+    y, bound = y[:, None].expand(N, c2), bound[:, None].expand(N, c2)
+    close(dyra.dyra_linear(x.cuda(), w.cuda(), act="gelu", out_dtype=o), y, bound)
+    if dtype == out:
+        one = torch.ones(c2, dtype=t, device="cuda")
+        close(dyra.dyra_gated(x.cuda(), w.cuda(), zero.cuda(), bias_u=one, act="gelu"), y, bound, "gated")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gelu_of_experts_is_right_where_it_is_small(dtype):
+    """One inner feature of gelu(v) * 1, taken to every output by ones: its two bfloat16 parts leave out 2^-16 of it."""
+    import torch
+    t = types()[dtype]
+    T, c, f = 100, 16, 24
+    v = torch.linspace(-12.75, 6, T).to(t)
+    x = torch.zeros(T, c, dtype=t)
+    x[:, 0], x[:, 1] = v, 1
+    wg, wu, wd = torch.zeros(1, f, c, dtype=t), torch.zeros(1, f, c, dtype=t), torch.zeros(1, c, f, dtype=t)
+    wg[0, 3, 0], wu[0, 3, 1], wd[0, :, 3] = 1, 1, 1
+    y = dyra.dyra_moe(x.cuda(), wg.cuda(), wu.cuda(), wd.cuda(), torch.zeros(T, 1, dtype=torch.int32).cuda(),
+                      torch.ones(T, 1).cuda(), act="gelu")
+    ref, bound = gelu_bound(v, t)
+    ref, bound = ref[:, None].expand(T, c), bound[:, None].expand(T, c)
+    close(y, ref, bound + (2.0 ** -16 * ref.abs() if dtype == "bf16" else 0))
+
+
+@pytest.mark.parametrize("N", [3, 100])
+def test_gelu_of_infinity_and_nan(N):
+    import torch
+    x, w = torch.zeros(N, 8, dtype=torch.bfloat16), torch.zeros(40, 8, dtype=torch.bfloat16)
+    x[:, 0], w[:, 0] = 1, 1
+    x[0, 0], x[1, 0] = float("inf"), float("nan")
+    for o in (torch.bfloat16, torch.float32):
+        y = dyra.dyra_linear(x.cuda(), w.cuda(), act="gelu", out_dtype=o)
+        assert (y[0] == float("inf")).all() and y[1].isnan().all() and y[2:].isfinite().all()

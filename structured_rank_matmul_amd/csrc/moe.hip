@@ -131,7 +131,12 @@ __global__ __launch_bounds__(256) void route_kernel(const E *__restrict__ logits
     float weight = 0.f;
     if (at >= 0) {
         const float l = key_value(chosen);
-        weight = sigmoid ? 1.f / (1.f + expf(-l)) : (chosen == top ? 1.f : expf(l - largest)) / sum;
+        // The score.  To be renormalised a sigmoid of rows below 0 is taken relative to
+        // the row's largest, s(l) / s(m) = exp(l - m) (1 + exp(m)) / (1 + exp(l)): below
+        // -88 the scores themselves are 0 in float32, their ratios are not.
+        if (!sigmoid) weight = (chosen == top ? 1.f : expf(l - largest)) / sum;
+        else if (renormalise && largest < 0.f) weight = (chosen == top ? 1.f : expf(l - largest)) * (1.f + expf(largest)) / (1.f + expf(l));
+        else weight = 1.f / (1.f + expf(-l));
     }
     if (renormalise) {
         const float total = lane_sum<LANES>(weight);

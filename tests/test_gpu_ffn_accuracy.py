@@ -142,3 +142,29 @@ def test_gelu_of_infinity_and_nan(N):
     for o in (torch.bfloat16, torch.float32):
         y = dyra.dyra_linear(x.cuda(), w.cuda(), act="gelu", out_dtype=o)
         assert (y[0] == float("inf")).all() and y[1].isnan().all() and y[2:].isfinite().all()
+
+
+# ------------------------------------------------------------------ router
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(6, 8, 2), (9, 64, 8), (5, 200, 5), (4, 300, 20), (3, 1024, 64)])
+def test_sigmoid_scores_of_low_logits_are_renormalised(T, E, k, dtype):
+    """Scores below float32's range (logits under -88) have ratios all the same.  Bound as for the softmax: exponents of
+    at most 40 to 44 u each, k terms, quotients."""
+    import torch
+    logits = rand((T, E), 11, types()[dtype], 2.0).double()
+    logits += torch.tensor([-95.0, -200.0, -3.0, -1e4, 2.0, -88.0, -60.0, 0.0, -104.0])[:T, None]
+    logits = logits.to(types()[dtype])
+    logits[1, k:] = -float("inf")                 # fewer left than places
+    logits[1, 0] = -float("inf")
+    ids, w = dyra.dyra_route(logits.cuda(), k, score="sigmoid", scale=1.5)
+    l = logits.double()
+    order = torch.from_numpy((-l.numpy()).argsort(axis=1, kind="stable")[:, :k].copy())
+    top = l.gather(1, order)
+    s = torch.where(top == -float("inf"), top, torch.nn.functional.logsigmoid(top))
+    ref = 1.5 * torch.softmax(s, dim=1)
+    assert (ids.cpu() == torch.where(top == -float("inf"), -1, order).int()).all()
+    close(w, ref, (2 * 44 + k + 16) * 2 * U * ref)
+    lowest = torch.full((2, E), torch.finfo(types()[dtype]).min, dtype=types()[dtype], device="cuda")
+    equal = torch.full((2, k), 1 / k, dtype=torch.float64)
+    close(dyra.dyra_route(lowest, k, score="sigmoid")[1], equal, 4 * U * equal)

@@ -307,7 +307,8 @@ dyra_status dyra_dense_ref(const void *X, const void *Wt, int64_t N, int64_t c1,
  * to the current device and to the device of the pointers, allocates nothing
  * and does not synchronise, so it may be captured into a graph.  An output must
  * not overlap an input, except that Y may be the residual itself (same pointer
- * and row stride); an output at the address of another input is DYRA_ERR_ARG.
+ * and row stride); an output or a workspace at the address of another argument is
+ * DYRA_ERR_ARG.
  */
 typedef enum {
     DYRA_ACT_NONE = 0,

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/dyra.h"
 #include "ffn_kernels.h"
@@ -39,12 +40,14 @@ bool known(dyra_dtype t) { return t == DYRA_BF16 || t == DYRA_F32; }
 size_t size_of(dyra_dtype t) { return t == DYRA_BF16 ? 2 : 4; }
 bool known_act(dyra_act a) { return a >= DYRA_ACT_NONE && a <= DYRA_ACT_SILU; }
 
-// Whether Y of several rows is also an input that other rows' results still
-// read: X, a weight, or a residual whose rows lie otherwise.
-bool overlaps(const void *Y, int64_t ldy, int64_t N, const void *X, const void *W0, const void *W1, const void *R,
-              int64_t ldr) {
-    return Y == X || Y == W0 || Y == W1 || (R == Y && N > 1 && ldr != ldy);
+// Whether an output (not null) is at the address of one of these.
+bool among(const void *out, std::initializer_list<const void *> inputs) {
+    for (const void *p : inputs)
+        if (p == out) return true;
+    return false;
 }
+// Whether Y of several rows is a residual whose rows lie otherwise.
+bool other_rows(const void *Y, int64_t ldy, int64_t N, const void *R, int64_t ldr) { return R == Y && N > 1 && ldr != ldy; }
 
 // The checks that the linear layer and the gated pair share.  DYRA_OK with
 // *empty set: nothing to do.
@@ -98,7 +101,7 @@ dyra_status dyra_linear(const void *X, int64_t ldx, const void *Wt, int64_t ldw,
     if (residual && ldr != 0 && ldr < c2) return DYRA_ERR_ARG;
     if (empty) return DYRA_OK;
     if (!aligned(residual, size_of(out_dtype))) return DYRA_ERR_ALIGN;
-    if (overlaps(Y, ldy, N, X, Wt, Wt, residual, ldr)) return DYRA_ERR_ARG;
+    if (among(Y, {X, Wt, bias}) || other_rows(Y, ldy, N, residual, ldr)) return DYRA_ERR_ARG;
     if (!residual) ldr = 0;
     if (dtype == DYRA_F32)
         return run_linear<float, float, false>(X, ldx, Wt, nullptr, ldw, N, c1, c2, bias, nullptr, act, residual, ldr, Y, ldy, stream);
@@ -113,7 +116,7 @@ dyra_status dyra_gated(const void *X, int64_t ldx, const void *Wg, const void *W
     bool empty;
     const dyra_status s = check_linear(X, ldx, Wg, Wu, ldw, N, c1, c2, dtype, bias_g, bias_u, act, H, ldh, dtype, &empty);
     if (s != DYRA_OK || empty) return s;
-    if (overlaps(H, ldh, N, X, Wg, Wu, nullptr, 0)) return DYRA_ERR_ARG;
+    if (among(H, {X, Wg, Wu, bias_g, bias_u})) return DYRA_ERR_ARG;
     if (dtype == DYRA_F32)
         return run_linear<float, float, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
     return run_linear<bf16, bf16, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
@@ -130,6 +133,7 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
     if (T == 0) return DYRA_OK;
     if (!logits || !ids || !weights) return DYRA_ERR_ARG;
     if (!aligned(logits, size_of(dtype)) || !aligned(ids, 4) || !aligned(weights, 4)) return DYRA_ERR_ALIGN;
+    if (among(ids, {logits, weights}) || among(weights, {logits})) return DYRA_ERR_ARG;
     hipStream_t st = (hipStream_t)stream;
     const bool sg = score == DYRA_SCORE_SIGMOID, rn = renormalise != 0;
     if (dtype == DYRA_BF16)
@@ -138,7 +142,8 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
 }
 
 size_t dyra_moe_workspace_bytes(int64_t T, int32_t topk, int64_t f, dyra_dtype dtype) {
-    if (T < 0 || topk < 1 || f < 1 || f > kMaxExpertRow || T > dyra::kMoeMaxPairs / topk || !known(dtype)) return 0;
+    if (T < 0 || topk < 1 || topk > 64 || f < 1 || f > kMaxExpertRow || T > dyra::kMoeMaxPairs / topk || !known(dtype)) return 0;
+    if (f % (16 / (int64_t)size_of(dtype)) != 0) return 0;
     return (size_t)T * (size_t)topk * (size_t)f * size_of(dtype);
 }
 
@@ -163,9 +168,8 @@ dyra_status dyra_moe(const void *X, int64_t ldx, int64_t T, int64_t c, int64_t f
     if (!workspace || workspace_bytes < dyra_moe_workspace_bytes(T, topk, f, dtype)) return DYRA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return DYRA_ERR_ALIGN;
     // Y over X is fine: X is read for the last time before Y is first written
-    if (overlaps(Y, ldy, T, nullptr, Wg, Wu, residual, ldr) || Y == Wd || workspace == Y || workspace == X ||
-        (workspace == residual))
-        return DYRA_ERR_ARG;
+    if (among(Y, {Wg, Wu, Wd, ids, weights}) || other_rows(Y, ldy, T, residual, ldr)) return DYRA_ERR_ARG;
+    if (among(workspace, {Y, X, Wg, Wu, Wd, ids, weights, residual})) return DYRA_ERR_ARG;
     const size_t inner = dyra_moe_workspace_bytes(T, topk, f, dtype);
     // what is there beyond the inner activations: room for split sums, then for what
     // the activations' rounding leaves out

@@ -609,7 +609,8 @@ def dyra_moe(X, Wg, Wu, Wd, ids, weights, act: str = "silu", residual=None, Y=No
     else:
         ldy = _matrix(Y, "Y", dev, T, c, t)
     if workspace is None:
-        workspace = _new((4 * T * topk * f + 8192 * T + 16,), torch.uint8, X, stream)
+        # (none for more pairs than a call takes: it is refused below)
+        workspace = _new((4 * T * topk * f + 8192 * T + 16 if T * topk <= 1024 else 0,), torch.uint8, X, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on GPU {dev}")
     status = (_lib or load()).dyra_moe(X.data_ptr(), ldx, T, c, f, g, u, d, experts, i, w, topk, _codes[t], code, r, ldr,

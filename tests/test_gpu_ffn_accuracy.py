@@ -168,3 +168,19 @@ def test_sigmoid_scores_of_low_logits_are_renormalised(T, E, k, dtype):
     lowest = torch.full((2, E), torch.finfo(types()[dtype]).min, dtype=types()[dtype], device="cuda")
     equal = torch.full((2, k), 1 / k, dtype=torch.float64)
     close(dyra.dyra_route(lowest, k, score="sigmoid")[1], equal, 4 * U * equal)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_too_many_pairs_are_refused_without_a_workspace():
+    """16384 tokens through 8 places of 14336 features would need 7.5 GB of it."""
+    import torch
+    T, k, c, f = 16384, 8, 8, 14336
+    x = torch.zeros(T, c, dtype=torch.bfloat16, device="cuda")
+    w, wd = torch.zeros(1, f, c, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, c, f, dtype=torch.bfloat16, device="cuda")
+    ids, p = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(dyra.DyraError) as err:
+        dyra.dyra_moe(x, w, w, wd, ids, p)
+    assert err.value.status == 2 and torch.cuda.max_memory_allocated() - before < 1 << 20

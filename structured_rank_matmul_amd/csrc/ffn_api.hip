@@ -21,19 +21,6 @@ constexpr int64_t kMaxRow = int64_t{1} << 20;
 // The same for the expert layer, whose pairs' rows (at most kMoeMaxPairs) are all
 // addressed from the first.
 constexpr int64_t kMaxExpertRow = int64_t{1} << 18;
-// Up to this many tokens the weights are streamed (launch_skinny).
-constexpr int64_t kSkinnyTokens = 32;
-// Whether X is streamed and the weights' rows take the tokens' part (launch_narrow):
-// few features, one unit of 16 tokens a CU; float32, where the tiles are bound by their
-// MFMAs, up to four with one block of features and two with two.  Tiles | narrow,
-// us: bf16 2048 x 4096 -> 32 13.4 | 8.9, 2048 x 7168 -> 8 21.2 | 7.9, 8192 x 4096 -> 32
-// 14.2 | 18.7; float32 1589 x 9184 -> 32 105 | 30, 16384 x 768 -> 10 16.8 | 11.5, 8000 x 2048
-// -> 32 26.3 | 20.1, 16384 x 768 -> 32 17.0 | 18.4.
-template <typename E, bool GATED> bool narrow(int64_t M, int64_t N) {
-    const int blocks = GATED || N > 16 ? 2 : 1;
-    return N <= (GATED ? 16 : 32) && M <= 16 * 256 * (sizeof(E) == 4 ? 4 / blocks : 1);
-}
-
 dyra_status hip_status(hipError_t e) { return e == hipSuccess ? DYRA_OK : DYRA_ERR_HIP; }
 bool aligned(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 bool known(dyra_dtype t) { return t == DYRA_BF16 || t == DYRA_F32; }
@@ -74,8 +61,8 @@ dyra_status check_linear(const void *X, int64_t ldx, const void *W0, const void 
 }
 
 template <typename E, typename O, bool GATED> dyra_status run(const dyra::LinearArgs<E, O> &a, hipStream_t st) {
-    if (a.M <= kSkinnyTokens) return hip_status(dyra::launch_skinny<E, O, GATED>(a, st));
-    if (narrow<E, GATED>(a.M, a.N)) return hip_status(dyra::launch_narrow<E, O, GATED>(a, st));
+    if (a.M <= dyra::kSkinnyTokens) return hip_status(dyra::launch_skinny<E, O, GATED>(a, st));
+    if (dyra::takes_narrow(sizeof(E), GATED, a.M, a.N)) return hip_status(dyra::launch_narrow<E, O, GATED>(a, st));
     return hip_status(dyra::launch_linear<E, O, GATED>(a, st));
 }
 

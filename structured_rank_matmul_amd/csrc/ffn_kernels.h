@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ffn_choice.h"
+
 namespace dyra {
 
 typedef __bf16 bf16;
@@ -60,11 +62,6 @@ template <typename E> struct MoeArgs {
     bool rest;         // of every 8 features what their rounding left out follows (bf16)
     float *parts;      // kMoePartBytes a token, workspace, or null
 };
-// Pairs (token, place) that one call takes.
-constexpr int kMoeMaxPairs = 1024;
-constexpr int kMoeMaxExperts = 1024;
-// Of split sums, a token: at most 256 workgroups of 8 features in float32.
-constexpr int kMoePartBytes = 256 * 8 * 4;
 template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st);
 
 }  // namespace dyra

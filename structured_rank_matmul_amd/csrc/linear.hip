@@ -239,43 +239,11 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Tile shapes by tokens and weight rows (gated: gate and up rows together), and
-// the time of a round of one tile per CU: per slab in bf16 and in float32 (ns; from
-// products of one and of four full rounds at K = 1024 and 4096; a slab is 64 bf16 or
-// 32 floats), and for the start and the epilogue.  What the
-// choice is worth, us by tile (128 x 256 | 192 | 224 | 256 x 256): 448 363 333 336 at
-// 14336 x 4096 -> 4096, 388 307 306 276 at 12288, 237 212 173 181 at 25728 x 4096 ->
-// 1024, 62 62 65 71 at 2048 x 4096 -> 4096 (the library's product: 330, 265, 166, 55).
-enum Tile { T32x64, T64x64, T64x128, T128x128, T128x256, T192x256, T224x256, T256x256 };
-struct TileCost {
-    int bm, bn;
-    double slab, slab_f32, once;
-};
-constexpr TileCost kTiles[] = {{32, 64, 150, 345, 2500},    {64, 64, 230, 520, 2500},  {64, 128, 305, 1015, 3500},
-                               {128, 128, 550, 1905, 4000}, {128, 256, 870, 0, 5500},  {192, 256, 1110, 0, 4000},
-                               {224, 256, 1220, 0, 5000},   {256, 256, 1340, 0, 6000}};
-
-// The shape with the smallest estimated time for a product of `rows` weight rows.
-template <typename E> Tile pick_tile(double M, double rows, double slabs) {
-    Tile best = T32x64;
-    double cost = 1e300;
-    for (int i = T32x64; i <= (sizeof(E) == 2 ? T256x256 : T128x128); ++i) {
-        const TileCost &t = kTiles[i];
-        const double rounds = std::ceil(std::ceil(M / t.bm) * std::ceil(rows / t.bn) / 256.0);
-        const double c = rounds * (slabs * (sizeof(E) == 2 ? t.slab : t.slab_f32) + t.once);
-        if (c < cost) {
-            cost = c;
-            best = (Tile)i;
-        }
-    }
-    return best;
-}
-
 }  // namespace
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    const Tile tile = pick_tile<E>((double)a.M, (double)a.N * (GATED ? 2 : 1), std::ceil((double)a.K * sizeof(E) / 128.0));
+    const Tile tile = pick_tile(sizeof(E), GATED, a.M, a.N, a.K * (int64_t)sizeof(E));
     if constexpr (sizeof(E) == 2) {
         if (tile == T256x256) return launch_big<O, GATED, 8>(a, st);
         if (tile == T224x256) return launch_big<O, GATED, 7>(a, st);

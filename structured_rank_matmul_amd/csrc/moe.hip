@@ -160,9 +160,6 @@ hipError_t launch_route_lanes(const E *logits, int64_t ld, int64_t T, int En, in
 
 // ------------------------------------------------------------------ expert layer
 
-// Pairs of one moe_down workgroup: 16 KB of sums.
-template <int ROWS> constexpr int kDownPairs = 4096 / ROWS;
-
 // The places of ids grouped by expert, in order, and cut into slots of at most
 // SLOT pairs of one expert: slot s holds pairs list[first[s] .. + count[s]) of
 // expert[s].  Every workgroup builds the same ones.
@@ -374,10 +371,10 @@ template <typename E, int SLABS> __global__ __launch_bounds__(kThreads) void moe
 // each token's places are added in order.
 template <int ROWS, int SLOT> struct DownLds {
     char ring[kWaves * kRingBytes];
-    float sums[kDownPairs<ROWS> * ROWS];  // of every pair
+    float sums[down_pairs(ROWS) * ROWS];  // of every pair
     float head[kWaves][16 * ROWS];        // of a run's first slot, begun by the run before
-    float weight[kDownPairs<ROWS>];
-    Slots<kDownPairs<ROWS>, SLOT> slots;
+    float weight[down_pairs(ROWS)];
+    Slots<down_pairs(ROWS), SLOT> slots;
 };
 // Slots hold SLOT pairs: of 8, the ring holds more weights; of 16, an expert of
 // more than 8 pairs is read once.  REST: H has two parts, which are rows 2 i and
@@ -540,22 +537,16 @@ template <typename E, int SLABS> hipError_t launch_up(const MoeArgs<E> &a, hipSt
     return hipGetLastError();
 }
 template <typename E, int ROWS, int SLOT, bool REST> hipError_t launch_down(const MoeArgs<E> &a, hipStream_t st) {
-    const int chunk = std::min(a.T, kDownPairs<ROWS> / a.k);
+    const int chunk = std::min(a.T, down_pairs(ROWS) / a.k);
     const int64_t rows = (a.c + ROWS - 1) / ROWS, chunks = (a.T + chunk - 1) / chunk;
-    // One workgroup streams about 50 bytes a ns.  The slabs are shared by as many as
-    // there are CUs for, down to 150 KB each, where that saves 8 us: the join takes 5
-    // and a launch more of the host.  57 tokens, 9 experts, 4 places, 360 x 5432: 98 ->
-    // 29 + 5 us; 10 tokens, 17 experts, 8 places, 296 x 1064: 15 -> 11 + 4.
-    const int64_t bytes = std::min<int64_t>(chunk * a.k, a.experts) * a.f * (int64_t)sizeof(E) * (ROWS + (REST ? 2 : 1) * SLOT);
-    const int64_t splits = std::min(256 / (rows * chunks), bytes / 150000);
-    const bool split = splits > 1 && a.parts && splits * a.c * 4 <= kMoePartBytes &&
-                       (double)bytes * (1 - 1.0 / (double)splits) > 400e3;
-    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT, REST>), dim3((unsigned)rows, (unsigned)chunks, split ? (unsigned)splits : 1u),
+    const int splits = down_splits({ROWS, SLOT}, sizeof(E), a.T, a.k, a.experts, a.c, a.f, a.parts != nullptr, REST);
+    const bool split = splits > 1;
+    hipLaunchKernelGGL((moe_down_kernel<E, ROWS, SLOT, REST>), dim3((unsigned)rows, (unsigned)chunks, (unsigned)splits),
                        dim3(kThreads), 0, st, a, chunk, split ? a.parts : nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !split) return e;
     hipLaunchKernelGGL((moe_join_kernel<E>), dim3((unsigned)((a.T * (a.c / 4) + 255) / 256)), dim3(256), 0, st, a, a.parts,
-                       (int)splits);
+                       splits);
     return hipGetLastError();
 }
 
@@ -576,24 +567,19 @@ hipError_t launch_route(const E *logits, int64_t ld, int64_t T, int En, int k, b
 
 template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st) {
     if (a.T <= 0) return hipSuccess;
-    const int pairs = a.T * a.k;
-    if (pairs > kMoeMaxPairs || a.experts > kMoeMaxExperts) return hipErrorInvalidValue;
-    const int slabs = (int)((a.c * (int64_t)sizeof(E) + 128 * kWaves - 1) / (128 * kWaves));  // of K, a wavefront's
-    const hipError_t e = slabs <= 2   ? launch_up<E, 2>(a, st)
-                         : slabs <= 4 ? launch_up<E, 4>(a, st)
-                         : slabs <= 8 ? launch_up<E, 8>(a, st)
+    if (a.T * a.k > kMoeMaxPairs || a.experts > kMoeMaxExperts) return hipErrorInvalidValue;
+    static_assert(kWaves == 8, "up_slabs divides c by it");
+    const int slabs = up_slabs(a.c * (int64_t)sizeof(E));
+    const hipError_t e = slabs == 2   ? launch_up<E, 2>(a, st)
+                         : slabs == 4 ? launch_up<E, 4>(a, st)
+                         : slabs == 8 ? launch_up<E, 8>(a, st)
                                       : launch_up<E, 12>(a, st);
     if (e != hipSuccess) return e;
-    // 8 rows a workgroup while that gives no more workgroups than CUs (each takes
-    // one), or where 16 would read the weights for a second chunk of tokens; else
-    // 16: 8 tokens, 32 experts, 4 places, 2880 x 1024 72 us against 86.  Slots of 8
-    // where experts have 4 pairs on average
-    const bool few = a.T <= 8 || pairs <= 6 * a.experts;
-    const bool eight = a.c <= 8 * 256 || pairs > kDownPairs<16>;
+    const Down d = down_kernel(a.T, a.k, a.experts, a.c);
     auto go = [&](auto rest) {
         constexpr bool REST = decltype(rest)::value;
-        if (eight) return few ? launch_down<E, 8, 8, REST>(a, st) : launch_down<E, 8, 16, REST>(a, st);
-        return few ? launch_down<E, 16, 8, REST>(a, st) : launch_down<E, 16, 16, REST>(a, st);
+        if (d.rows == 8) return d.slot == 8 ? launch_down<E, 8, 8, REST>(a, st) : launch_down<E, 8, 16, REST>(a, st);
+        return d.slot == 8 ? launch_down<E, 16, 8, REST>(a, st) : launch_down<E, 16, 16, REST>(a, st);
     };
     if constexpr (sizeof(E) == 2) {
         if (a.rest) return go(std::true_type{});

@@ -11,8 +11,6 @@
 // against 23.2; 32 tokens, 1024 -> 1024 5.0 against 7.2.
 #include "skinny.h"
 
-#include <algorithm>
-
 namespace dyra {
 
 namespace {
@@ -195,22 +193,23 @@ hipError_t launch_slabs(const LinearArgs<E, O> &a, int units, hipStream_t st) {
 
 template <typename E, typename O, bool GATED> hipError_t launch_skinny(const LinearArgs<E, O> &a, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    const int units = (int)((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
-    // registers hold a wavefront's slabs of the tokens (8 a slab and block of 16)
-    // up to 24 slabs of one block or 12 of two; they pay from the third unit of a
-    // workgroup on (two blocks: the second)
-    const int slabs = (int)((a.K * (int64_t)sizeof(E) + 128 * kWaves - 1) / (128 * kWaves));
-    if (a.M <= 16 && units > 512 && slabs <= 24) {
-        if (slabs <= 2) return launch_slabs<E, O, GATED, 2, 1>(a, units, st);
-        if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 1>(a, units, st);
-        if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 1>(a, units, st);
-        if (slabs <= 16) return launch_slabs<E, O, GATED, 16, 1>(a, units, st);
-        return launch_slabs<E, O, GATED, 24, 1>(a, units, st);
-    }
-    if (a.M > 16 && a.M <= 32 && units > 256 && slabs <= 12) {
-        if (slabs <= 4) return launch_slabs<E, O, GATED, 4, 2>(a, units, st);
-        if (slabs <= 8) return launch_slabs<E, O, GATED, 8, 2>(a, units, st);
-        return launch_slabs<E, O, GATED, 12, 2>(a, units, st);
+    const int units = (int)few_token_units(GATED, a.N);
+    const FewTokens few = few_tokens(GATED, a.M, a.N, a.K * (int64_t)sizeof(E));
+    static_assert(kWaves == 8, "few_tokens divides K by it");
+    if (few.blocks == 1) {
+        switch (few.slabs) {
+        case 2: return launch_slabs<E, O, GATED, 2, 1>(a, units, st);
+        case 4: return launch_slabs<E, O, GATED, 4, 1>(a, units, st);
+        case 8: return launch_slabs<E, O, GATED, 8, 1>(a, units, st);
+        case 16: return launch_slabs<E, O, GATED, 16, 1>(a, units, st);
+        case 24: return launch_slabs<E, O, GATED, 24, 1>(a, units, st);
+        }
+    } else {
+        switch (few.slabs) {
+        case 4: return launch_slabs<E, O, GATED, 4, 2>(a, units, st);
+        case 8: return launch_slabs<E, O, GATED, 8, 2>(a, units, st);
+        case 12: return launch_slabs<E, O, GATED, 12, 2>(a, units, st);
+        }
     }
     hipLaunchKernelGGL((skinny_ring_kernel<E, O, Units<E, O, GATED>>), dim3(workgroups(units)), dim3(kThreads), 0, st, a,
                        units, (int)((a.M + 15) / 16));

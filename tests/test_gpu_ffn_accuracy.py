@@ -184,3 +184,26 @@ def test_too_many_pairs_are_refused_without_a_workspace():
     with pytest.raises(dyra.DyraError) as err:
         dyra.dyra_moe(x, w, w, wd, ids, p)
     assert err.value.status == 2 and torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+# ------------------------------------------------------------------ silu where it is small
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("N,c2", [(7, 48), (16, 8200), (300, 8), (300, 70), (4000, 2050)])
+def test_silu_is_right_where_it_is_small(N, c2, dtype, out):
+    """silu(-87) is -1.4e-36.  In float32 exp is right to 4 u, the reciprocal to 2 u, the sum and the product to u each: 8 u
+    in all.  For bfloat16 results exp's argument is right to 2 u |v| and the rest to 8 u."""
+    import torch
+    t, o = types()[dtype], types()[out]
+    v = torch.linspace(-87, 6, N).to(t)
+    x, w, zero = torch.zeros(N, 8, dtype=t), torch.zeros(c2, 8, dtype=t), torch.zeros(c2, 8, dtype=t)
+    x[:, 2], w[:, 2] = v, 1
+    v = v.double()
+    y = v / (1 + torch.exp(-v))
+    own = (8 * U + (2 * U * v.abs() if out == "bf16" else 0)) * y.abs()
+    bound = own + half(o) * (y.abs() + own)
+    y, bound = y[:, None].expand(N, c2), bound[:, None].expand(N, c2)
+    close(dyra.dyra_linear(x.cuda(), w.cuda(), act="silu", out_dtype=o), y, bound)
+    if dtype == out:
+        one = torch.ones(c2, dtype=t, device="cuda")
+        close(dyra.dyra_gated(x.cuda(), w.cuda(), zero.cuda(), bias_u=one, act="silu"), y, bound, "gated")

@@ -1,11 +1,13 @@
 // Device building blocks shared by the feed-forward kernels: 16 x 16 MFMA
 // blocks 32 deep, activations, guarded 16-byte loads.
 //
-// Operands of one 16 x 16 block: lane l holds 8 contraction elements
-// k = 8 (l / 16) .. + 7 of row (first operand) or column (second operand)
-// l % 16.  For bf16 that is one v_mfma_f32_16x16x32_bf16; for float32 the same
-// 8 elements feed eight v_mfma_f32_16x16x4_f32 steps, step t contracting
-// element t of every lane group, the same permutation of k for both operands.
+// Operands of one 16 x 16 block: lane l holds 8 contraction elements of row
+// (first operand) or column (second operand) l % 16.  For bf16 these are k = 8 (l / 16)
+// .. + 7 of one v_mfma_f32_16x16x32_bf16.  For float32 they are k = 4 (l / 16) .. + 3
+// and 16 more of the same, and feed eight v_mfma_f32_16x16x4_f32 steps, step t
+// contracting element t of every lane group, the same permutation of k for both
+// operands.  (Chunks of 16 bytes g and 4 + g of a slab, as bf16 reads in its two steps: 2 g
+// and 2 g + 1 would meet on a bank under the same swizzle.)
 // Result (both): lane l holds column l % 16, register t row 4 (l / 16) + t.
 // The weights are always the first operand, so a lane's four registers are
 // four consecutive output features of one token.

@@ -131,8 +131,8 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
             if constexpr (sizeof(E) == 2) {
                 return *reinterpret_cast<const bf16x8 *>(row + (((4 * h + g) ^ swz) << 4));
             } else {
-                const f32x4 lo = *reinterpret_cast<const f32x4 *>(row + (((2 * g) ^ swz) << 4));
-                const f32x4 hi = *reinterpret_cast<const f32x4 *>(row + (((2 * g + 1) ^ swz) << 4));
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(row + ((g ^ swz) << 4));
+                const f32x4 hi = *reinterpret_cast<const f32x4 *>(row + (((4 + g) ^ swz) << 4));
                 return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         };

@@ -315,7 +315,7 @@ template <typename E> struct UpPosition {
         if (!fresh) return;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            w.off[q] = (uint32_t)(slab_row(q) & 7) * (uint32_t)(a->c * sizeof(E)) + slab_chunk(q);
+            w.off[q] = (uint32_t)(slab_row(q) & 7) * (uint32_t)(a->c * sizeof(E)) + slab_chunk();
     }
     __device__ __forceinline__ bool new_tokens() const { return tile == 0; }
     __device__ __forceinline__ int blocks() const { return pairs > 16 ? 2 : 1; }
@@ -431,11 +431,11 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs<E> a, int ch
         const int last = (int)min((int64_t)ROWS, a.c - c0) - 1, n = L.count[in_slot], f0 = L.first[in_slot];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            w.off[q] = (uint32_t)min(slab_row(q), last) * (uint32_t)row_bytes + slab_chunk(q);
+            w.off[q] = (uint32_t)min(slab_row(q), last) * (uint32_t)row_bytes + slab_chunk();
             // rows past the slot's pairs read nothing
             // REST: pairs 8 .. 15 in x2
             const int i = slab_row(q) / WIDE;
-            const uint32_t in_row = WIDE * slab_chunk(q) + (REST ? 16 * (slab_row(q) & 1) : 0);
+            const uint32_t in_row = WIDE * slab_chunk() + (REST ? 16 * (slab_row(q) & 1) : 0);
             x.off[q] = i < n ? (uint32_t)L.list[f0 + i] * (uint32_t)(WIDE * row_bytes) + in_row : kOutside;
             x2.off[q] = i + 8 < n ? (uint32_t)L.list[f0 + i + 8] * (uint32_t)(WIDE * row_bytes) + in_row : kOutside;
         }

@@ -5,9 +5,12 @@
 // A slab is 128 bytes of K of 16 rows, of weights or of tokens, copied by buffer
 // loads that write LDS: 8 rows of 128 bytes (whole cache lines) an instruction, no
 // registers held.  Row r keeps
-// chunk c (16 bytes) at position c ^ (r / 2 % 8), so the fragment reads are free
-// of bank conflicts; a chunk past the end of K is read out of the buffer's
-// range, which gives zeros.
+// chunk c (16 bytes) at position c ^ r % 8; a chunk past the end of K is read out of
+// the buffer's range, which gives zeros.  A 16-byte LDS read serves 16 lanes at a
+// time, lanes 0 .. 3, 12 .. 15 and 20 .. 27 (of rows 0 .. 3, 12 .. 15 and 4 .. 11, two
+// chunks) first: these positions fall on distinct banks, of 16 rows and of 8.  What
+// conflicts the counters still show (15 to 43 % of LDS cycles in the kernels of few
+// positions a workgroup) are those of the wavefronts' sums, written 16 bytes a lane.
 //
 // This pattern alone, without the tokens and the products, streams 235 MB of
 // 8 KB rows in 38.4 us (6.1 TB/s); the best plain register stream of the same
@@ -22,9 +25,9 @@ namespace dyra {
 // This lane's part of the copies of 16 rows: row 8 q + lane / 8, q = 0, 1, and
 // the chunk (byte offset) that the swizzle puts at its place.
 __device__ __forceinline__ int slab_row(int q) { return 8 * q + ((threadIdx.x & 63) >> 3); }
-__device__ __forceinline__ uint32_t slab_chunk(int q) {
+__device__ __forceinline__ uint32_t slab_chunk() {
     const int lane = threadIdx.x & 63;
-    return 16u * (((lane & 7) ^ (lane >> 4)) ^ (4 * q));
+    return 16u * ((lane & 7) ^ (lane >> 3));
 }
 // Where 16 rows lie: the buffer of rows 8 q .. and this lane's offset in it.
 struct SlabRows {
@@ -45,15 +48,15 @@ __device__ __forceinline__ f32x4 slab_product(f32x4 acc, const SlabFrag<float> &
 }
 // The fragments of row `lane % ROWS` of a slab in LDS.
 template <typename E, int ROWS> __device__ __forceinline__ SlabFrag<E> slab_read(const char *slab) {
-    const int lane = threadIdx.x & 63, r16 = lane & (ROWS - 1), g = lane >> 4, sw = r16 >> 1;
+    const int lane = threadIdx.x & 63, r16 = lane & (ROWS - 1), g = lane >> 4, sw = r16 & 7;
     const char *p = slab + r16 * 128;
     SlabFrag<E> r;
     if constexpr (sizeof(E) == 2) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) r.f[h] = *reinterpret_cast<const bf16x8 *>(p + (((4 * h + g) ^ sw) << 4));
     } else {
-        const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + (((2 * g) ^ sw) << 4));
-        const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + (((2 * g + 1) ^ sw) << 4));
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + ((g ^ sw) << 4));
+        const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + (((4 + g) ^ sw) << 4));
         r.f[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return r;
@@ -72,7 +75,7 @@ template <typename E> __device__ __forceinline__ SlabFrag<E> slab_load(__amdgpu_
 #pragma unroll
         for (int h = 0; h < 2; ++h) r.f[h] = __builtin_bit_cast(bf16x8, chunk(4 * h + g));
     } else {
-        const f32x4 lo = __builtin_bit_cast(f32x4, chunk(2 * g)), hi = __builtin_bit_cast(f32x4, chunk(2 * g + 1));
+        const f32x4 lo = __builtin_bit_cast(f32x4, chunk(g)), hi = __builtin_bit_cast(f32x4, chunk(4 + g));
         r.f[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return r;
@@ -96,7 +99,7 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
     template <int ROWS> __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
 #pragma unroll
         for (int q = 0; q < ROWS / 8; ++q)
-            buffer_to_lds16(r.buf[q], (int)slab_chunk(q) < left ? r.off[q] : kOutside, k, dst + 1024 * q);
+            buffer_to_lds16(r.buf[q], (int)slab_chunk() < left ? r.off[q] : kOutside, k, dst + 1024 * q);
     }
     // Copies one slab at byte `k` of the rows; `left` bytes of the rows are left.
     __device__ __forceinline__ void issue(const SlabRows &w, uint32_t k, int left) { issue(w, w, k, left); }

@@ -28,7 +28,7 @@ template <typename E, typename O, bool GATED> struct Units {
         if (!fresh) return;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            w.off[q] = (uint32_t)(GATED ? slab_row(q) & 7 : slab_row(q)) * (uint32_t)(a->ldw * sizeof(E)) + slab_chunk(q);
+            w.off[q] = (uint32_t)(GATED ? slab_row(q) & 7 : slab_row(q)) * (uint32_t)(a->ldw * sizeof(E)) + slab_chunk();
     }
     // What goes through the ring beside them: tokens 16 group ..
     static constexpr bool kPaired = false;
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void skinny_ring_kernel(LinearArgs<E, O> 
     SlabRows w, x;
     const uint32_t xld = (uint32_t)(U.other_ld() * sizeof(E));
 #pragma unroll
-    for (int q = 0; q < 2; ++q) x.off[q] = (uint32_t)slab_row(q) * xld + slab_chunk(q);
+    for (int q = 0; q < 2; ++q) x.off[q] = (uint32_t)slab_row(q) * xld + slab_chunk();
     int in_unit = s0 < s1 ? (int)blockIdx.x : units, in_group = 0, in_slab = s0;
     auto aim_tokens = [&]() __attribute__((always_inline)) { x.buf[0] = x.buf[1] = U.other(in_group); };
     U.weights(min(in_unit, units - 1), w, true);
@@ -153,7 +153,7 @@ template <typename E, typename O, bool GATED> struct NarrowUnits {
         w.buf[0] = w.buf[1] = panel(a->X + from, ((a->M - 1) * a->ldx + a->K - from) * (int64_t)sizeof(E));
         if (!fresh) return;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w.off[q] = (uint32_t)slab_row(q) * (uint32_t)(a->ldx * sizeof(E)) + slab_chunk(q);
+        for (int q = 0; q < 2; ++q) w.off[q] = (uint32_t)slab_row(q) * (uint32_t)(a->ldx * sizeof(E)) + slab_chunk();
     }
     static constexpr bool kPaired = GATED;
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t other(int group) const {

@@ -389,7 +389,7 @@ dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t expert
  * workspace device, >= dyra_moe_workspace_bytes(T, topk, f, dtype) bytes,
  *           contents on entry ignored; calls that overlap in time need separate
  *           ones.  It holds the experts' inner activations in dtype.  With
- *           8192 bytes more for each token, layers of c < 2048 may share the
+ *           8192 bytes more for each token, layers of c <= 1024 may share the
  *           second product's f among workgroups (faster; the sums run in another
  *           order).  With T * topk * f * 2 bytes more beyond those, the inner
  *           activations of bfloat16 layers keep 16 bits of mantissa between the

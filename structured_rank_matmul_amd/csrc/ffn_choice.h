@@ -43,10 +43,15 @@ inline FewTokens few_tokens(bool gated, int64_t M, int64_t N, int64_t row_bytes)
     return {0, 1};
 }
 
-// Tile shapes by tokens and weight rows (gated: gate and up rows together), and
-// the time of a round of one tile per CU: per slab in bf16 and in float32 (ns; from
-// products of one and of four full rounds at K = 1024 and 4096; a slab is 64 bf16 or
-// 32 floats), and for the start and the epilogue.  What the
+// Tile shapes by tokens and weight rows (gated: gate and up rows together), and the
+// time of a round of one tile per CU: per slab in bf16 and in float32 (ns; a slab is 64
+// bf16 or 32 floats of K), and for the start and the epilogue.  From whole calls of one
+// and of four full rounds at K = 1024 and 4096, plain and gated, reads from memory
+// included; taken again, bf16: 174 to 196, 193 to 282, 290 to 342, 512 to 605, 854 to
+// 892, 1092 to 1142, 1190 to 1231, 1332 to 1338; float32: 345 to 369, 492 to 563, 995 to
+// 1093, 1861 to 1955.  The first stays at 150: with 185, 40 random shapes whose choice
+// that changes (64 x 64 for 32 x 64) ran 10 % slower.  What every tile reads alike, the
+// operands once, is left out: at 64 x 4096 -> 2 x 14336 that is half of the time.  What the
 // choice is worth, us by tile (128 x 256 | 192 | 224 | 256 x 256): 448 363 333 336 at
 // 14336 x 4096 -> 4096, 388 307 306 276 at 12288, 237 212 173 181 at 25728 x 4096 ->
 // 1024, 62 62 65 71 at 2048 x 4096 -> 4096 (the library's product: 330, 265, 166, 55).

@@ -27,7 +27,8 @@
 // the 32-deep steps in turn on larger parts of the tile (64 x 64: 32 KB), and add
 // their sums through LDS at the end: bf16 slabs of 32 x 64, 64 x 64, 64 x 128, 128 x
 // 128 and 128 x 256 tiles take 149, 179, 291, 498 and 830 ns where one group of
-// smaller parts took 163, 194, 349, 549 and 913.
+// smaller parts took 163, 194, 349, 549 and 913.  (Operands in the L2s; from memory see
+// ffn_choice.h.)
 #include "linear_big.h"
 
 #include <algorithm>

@@ -12,18 +12,19 @@
 // the weights streamed through per-wavefront rings (skinny.h).  Every workgroup
 // sorts the places by expert itself (a few LDS steps), so that two launches do.  No
 // atomics on results: every pair's products have a place of their own in LDS and
-// are added per token in the order of its places.  Up and down take 141 and 81 us
-// for 48 tokens with 6 places over 64 experts of 2048 x 1408 (1.08 GB, 4.9 TB/s),
-// 318 and 168 for 16 tokens with 2 over 8 of 4096 x 14336 (2.8 GB, 5.7 TB/s), 17.8
-// and 11.8 for 1 token with 8 over 64 of 2048 x 1024 (101 MB, start-up included).
+// are added per token in the order of its places.  Up and down take 137 and 77 us
+// for 48 tokens with 6 places over 64 experts of 2048 x 1408 (1.08 GB, 5.0 TB/s),
+// 326 and 170 for 16 tokens with 2 over 8 of 4096 x 14336 (2.8 GB, 5.7 TB/s), 18.0
+// and 10.7 for 1 token with 8 over 64 of 2048 x 1024 (101 MB, start-up included);
+// float32, 48 tokens with 6 over 64 of 2048 x 704 (1.1 GB) 135 and 80.
 //
 // H between the two is a bf16 operand of the second product.  Rounded to it once,
 // it alone puts 1e-3 of a result's size into every result, where the last rounding
 // puts 1.66e-3 (error against float64, 16 tokens with 2 places over 8 experts of
 // 4096 x 14336: 2.00e-3 against 1.66e-3).  So H keeps what the rounding left out as
 // a second bf16 (together to 2^-16 of it), and the second product is taken of both
-// parts: twice the ring bytes of the pairs, 0.5, 11 and 7 us in the cases above, 20
-// of 88 at 512 tokens with 2 places over 8 experts of 1024 x 2816.  A caller whose
+// parts: twice the ring bytes of the pairs, 10, 4 and 0.5 us of a call in the cases
+// above, 34 of 192 at 512 tokens with 2 places over 8 experts of 1024 x 2816.  A caller whose
 // workspace has no room for the second part has H rounded once.
 #include "lanes.h"
 #include "skinny.h"

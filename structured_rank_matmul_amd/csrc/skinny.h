@@ -8,9 +8,10 @@
 // chunk c (16 bytes) at position c ^ r % 8; a chunk past the end of K is read out of
 // the buffer's range, which gives zeros.  A 16-byte LDS read serves 16 lanes at a
 // time, lanes 0 .. 3, 12 .. 15 and 20 .. 27 (of rows 0 .. 3, 12 .. 15 and 4 .. 11, two
-// chunks) first: these positions fall on distinct banks, of 16 rows and of 8.  What
-// conflicts the counters still show (15 to 43 % of LDS cycles in the kernels of few
-// positions a workgroup) are those of the wavefronts' sums, written 16 bytes a lane.
+// chunks) first: these positions fall on distinct banks, of 16 rows and of 8.  The
+// conflicts that the counters show in skinny_kernel, skinny_ring_kernel and
+// moe_up_kernel (15 to 43 % of LDS cycles) are those of the wavefronts' sums, which
+// are written 16 bytes a lane.
 //
 // This pattern alone, without the tokens and the products, streams 235 MB of
 // 8 KB rows in 38.4 us (6.1 TB/s); the best plain register stream of the same

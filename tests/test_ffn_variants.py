@@ -12,7 +12,7 @@ def choice(tmp_path_factory):
 
 TOKENS = [1, 8, 16, 17, 32, 33, 64, 100, 128, 200, 256, 400, 700, 1000, 1024, 1500, 2048, 3000, 4096, 5000, 8000, 12000, 16384, 30000, 65536]
 FEATURES = [1, 8, 16, 17, 30, 32, 33, 64, 100, 200, 400, 800, 1024, 1300, 2048, 2100, 3000, 4096, 4200, 6000, 8200, 12000, 20000]
-BYTES = [16, 128, 512, 1024, 2048, 3000 // 16 * 16, 4096, 6144, 8192, 12288, 16384, 20480, 24576, 30720, 65536]
+BYTES = [16, 128, 512, 1024, 2048, 3000 // 16 * 16, 4096, 6144, 8192, 12288, 16384, 20480, 24576, 28672, 65536]
 
 
 @pytest.mark.parametrize("gated", [False, True])

@@ -349,6 +349,73 @@ dyra_status dyra_gated(const void *X, int64_t ldx, const void *Wg, const void *W
                        int64_t c1, int64_t c2, dyra_dtype dtype, const void *bias_g, const void *bias_u,
                        dyra_act act, void *H, int64_t ldh, void *stream);
 
+/*
+ * The same layer in 8-bit integers: rows of int8 with a float32 scale each stand for
+ * the values Q[i][j] scales[i].  Rows of activations have one scale a token, rows of
+ * weights (nn.Linear layout) one an output feature.  c, c1 <= 65536.
+ *
+ * Root-mean-square norm of every row, after a residual's addition:
+ *
+ *     Z = X + residual,   S = Z,   Y = Z / sqrt(mean(Z^2) + eps) * weight
+ *
+ * X         device, dtype, [N][c], c any number >= 1.
+ * residual  device, dtype, [N][c], or NULL; ldr = 0 adds the same row to every token.
+ * weight    device, dtype, [c], or NULL for ones.
+ * eps       at least 2^-126 (the smallest normal float32), finite.
+ * S         device, dtype, [N][c], or NULL; may be the residual itself (same pointer
+ *           and row stride).
+ * Y         device, dtype, [N][c]; may be X itself (same pointer and row stride).
+ * Z is not rounded before it is normed.  A row that holds an infinity or a NaN gives
+ * what the formula gives: 0 and NaN.  All pointers are aligned to their elements.
+ */
+dyra_status dyra_norm(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, const void *residual, int64_t ldr,
+                      const void *weight, float eps, void *S, int64_t lds, void *Y, int64_t ldy, void *stream);
+
+/*
+ * dyra_norm with its result in 8 bits: Q device int8 [N][c] and scales device float32
+ * [N] as dyra_quantize gives them of Y, which is not rounded in between.
+ */
+dyra_status dyra_norm_quantize(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, const void *residual,
+                               int64_t ldr, const void *weight, float eps, void *S, int64_t lds, int8_t *Q, int64_t ldq,
+                               float *scales, void *stream);
+
+/*
+ * Rows in 8 bits: scales[i] = max(max_j |X[i][j]|, 127 * 2^-126) / 127 and Q[i][j] the whole
+ * number nearest to X[i][j] / scales[i] (-127 .. 127; next to the middle of two either one).
+ * A row of zeros has the scale 2^-126.  A row with an infinity or a NaN (for
+ * dyra_norm_quantize also one where Z * weight leaves float32's range) has the scale NaN
+ * and the values 0, so that what is made of it is NaN.  X device, dtype, [N][c], aligned to
+ * its elements; Q device int8 [N][c]; scales device float32 [N].
+ */
+dyra_status dyra_quantize(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, int8_t *Q, int64_t ldq,
+                          float *scales, void *stream);
+
+/* The values that rows in 8 bits stand for: X[i][j] = Q[i][j] * scales[i], X device, dtype, [N][c]. */
+dyra_status dyra_dequantize(const int8_t *Q, int64_t ldq, const float *scales, int64_t N, int64_t c, dyra_dtype dtype, void *X,
+                            int64_t ldx, void *stream);
+
+/*
+ * dyra_linear on 8-bit integers: Y = act(x_scales[i] w_scales[j] sum_k X[i][k] Wt[j][k] +
+ * bias[j]) + residual.  X device int8 [N][c1], Wt device int8 [c2][c1], any values -128 ..
+ * 127; x_scales device float32 [N], w_scales device float32 [c2]; bias device, out_dtype,
+ * [c2], or NULL; residual and Y device, out_dtype, [N][c2].  The sums are exact, in 32-bit
+ * integers.  c1, ldx and ldw are multiples of 16 (DYRA_ERR_SHAPE, DYRA_ERR_ALIGN), ldx, ldw
+ * <= 2^20; everything else as for dyra_linear.
+ */
+dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wt, int64_t ldw,
+                                  const float *w_scales, int64_t N, int64_t c1, int64_t c2, const void *bias, dyra_act act,
+                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *stream);
+
+/*
+ * dyra_gated on 8-bit integers: both products of H = act(X Wg + bias_g) * (X Wu + bias_u) as
+ * in dyra_linear_quantized, Wg with the scales g_scales, Wu with u_scales; biases and H in
+ * out_dtype.
+ */
+dyra_status dyra_gated_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wg, const float *g_scales,
+                                 const int8_t *Wu, const float *u_scales, int64_t ldw, int64_t N, int64_t c1, int64_t c2,
+                                 const void *bias_g, const void *bias_u, dyra_act act, dyra_dtype out_dtype, void *H,
+                                 int64_t ldh, void *stream);
+
 typedef enum {
     DYRA_SCORE_SOFTMAX = 0,  /* exp(l_e) / sum over all experts */
     DYRA_SCORE_SIGMOID = 1   /* 1 / (1 + exp(-l_e)) */

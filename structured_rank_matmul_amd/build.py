@@ -13,7 +13,7 @@ OUT = os.path.join(PKG, "libdyra.so")
 BUILD = os.path.join(ROOT, "_build")
 
 HIP_SOURCES = ["dyra_api.hip", "gemm.hip", "solve.hip", "dyra_decode.hip", "als.hip", "ns.hip", "blast.hip",
-               "ffn_api.hip", "linear.hip", "skinny.hip", "moe.hip"]
+               "ffn_api.hip", "linear.hip", "linear_i8.hip", "skinny.hip", "skinny_i8.hip", "rows.hip", "moe.hip"]
 CXX_SOURCES = ["host_factorize.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

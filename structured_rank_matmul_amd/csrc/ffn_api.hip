@@ -2,6 +2,7 @@
 // launcher.  Nothing is enqueued unless every check passes.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -11,6 +12,7 @@
 namespace {
 
 using dyra::bf16;
+using dyra::i8;
 
 // Tokens, output features: the launches of any such sizes whose outputs fit the
 // card have less than 2^32 threads.
@@ -21,16 +23,19 @@ constexpr int64_t kMaxRow = int64_t{1} << 20;
 // The same for the expert layer, whose pairs' rows (at most kMoeMaxPairs) are all
 // addressed from the first.
 constexpr int64_t kMaxExpertRow = int64_t{1} << 18;
+// Elements of a row in 8 bits: a sum of that many products of 128 * 128 is below 2^31,
+// and a workgroup of the row kernels holds that many.
+constexpr int64_t kMaxRow8 = int64_t{1} << 16;
 dyra_status hip_status(hipError_t e) { return e == hipSuccess ? DYRA_OK : DYRA_ERR_HIP; }
 bool aligned(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 bool known(dyra_dtype t) { return t == DYRA_BF16 || t == DYRA_F32; }
 size_t size_of(dyra_dtype t) { return t == DYRA_BF16 ? 2 : 4; }
 bool known_act(dyra_act a) { return a >= DYRA_ACT_NONE && a <= DYRA_ACT_SILU; }
 
-// Whether an output (not null) is at the address of one of these.
+// Whether an output is at the address of one of these.
 bool among(const void *out, std::initializer_list<const void *> inputs) {
     for (const void *p : inputs)
-        if (p == out) return true;
+        if (out && p == out) return true;
     return false;
 }
 // Whether Y of several rows is a residual whose rows lie otherwise.
@@ -58,6 +63,57 @@ dyra_status check_linear(const void *X, int64_t ldx, const void *W0, const void 
     if (!aligned(X, 16) || !aligned(W0, 16) || !aligned(W1, 16)) return DYRA_ERR_ALIGN;
     if (!aligned(Y, size_of(out)) || !aligned(b0, size_of(dtype)) || !aligned(b1, size_of(dtype))) return DYRA_ERR_ALIGN;
     return DYRA_OK;
+}
+
+// The checks that the products of 8-bit integers share.
+dyra_status check_quantized(const void *X, int64_t ldx, const void *sx, const void *W0, const void *W1, int64_t ldw,
+                            const void *s0, const void *s1, int64_t N, int64_t c1, int64_t c2, const void *b0, const void *b1,
+                            dyra_act act, const void *Y, int64_t ldy, dyra_dtype out, bool *empty) {
+    *empty = false;
+    if (!known(out)) return DYRA_ERR_DTYPE;
+    if (!known_act(act)) return DYRA_ERR_ARG;
+    if (N < 0 || c1 <= 0 || c2 <= 0 || N > kMaxDim || c2 > kMaxDim) return DYRA_ERR_SHAPE;
+    if (c1 > kMaxRow8 || c1 % 16 != 0 || ldx > kMaxRow || ldw > kMaxRow) return DYRA_ERR_SHAPE;
+    if (ldx < c1 || ldw < c1 || ldy < c2) return DYRA_ERR_ARG;
+    if (ldx % 16 != 0 || ldw % 16 != 0) return DYRA_ERR_ALIGN;
+    if (N == 0) {
+        *empty = true;
+        return DYRA_OK;
+    }
+    if (!X || !W0 || !W1 || !sx || !s0 || !s1 || !Y) return DYRA_ERR_ARG;
+    if (!aligned(X, 16) || !aligned(W0, 16) || !aligned(W1, 16)) return DYRA_ERR_ALIGN;
+    if (!aligned(sx, 4) || !aligned(s0, 4) || !aligned(s1, 4)) return DYRA_ERR_ALIGN;
+    if (!aligned(Y, size_of(out)) || !aligned(b0, size_of(out)) || !aligned(b1, size_of(out))) return DYRA_ERR_ALIGN;
+    return DYRA_OK;
+}
+
+// The checks that the calls on rows share: rows of `in` to rows of `out`.
+dyra_status check_rows(const void *in, int64_t ld_in, int64_t N, int64_t c, dyra_dtype dtype, const void *out, int64_t ld_out,
+                       bool *empty) {
+    *empty = false;
+    if (!known(dtype)) return DYRA_ERR_DTYPE;
+    if (N < 0 || c <= 0 || N > kMaxDim || c > kMaxRow8) return DYRA_ERR_SHAPE;
+    if (ld_in < c || ld_out < c) return DYRA_ERR_ARG;
+    if (N == 0) {
+        *empty = true;
+        return DYRA_OK;
+    }
+    return in && out ? DYRA_OK : DYRA_ERR_ARG;
+}
+dyra_status check_norm(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, const void *R, int64_t ldr,
+                       const void *W, float eps, const void *S, int64_t lds, const void *Y, int64_t ldy, bool *empty) {
+    if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return DYRA_ERR_ARG;
+    const dyra_status s = check_rows(X, ldx, N, c, dtype, Y, ldy, empty);
+    if (s != DYRA_OK) return s;
+    if ((R && ldr != 0 && ldr < c) || (S && lds < c)) return DYRA_ERR_ARG;
+    for (const void *p : {X, R, W, S})
+        if (!aligned(p, size_of(dtype))) return DYRA_ERR_ALIGN;
+    return DYRA_OK;
+}
+template <typename E>
+dyra::RowArgs<E> row_args(const void *X, int64_t ldx, int64_t N, int64_t c, const void *R, int64_t ldr, const void *W, float eps,
+                          void *S, int64_t lds, void *Y, int64_t ldy, float *scales) {
+    return {(const E *)X, ldx, (const E *)R, R ? ldr : 0, (const E *)W, N, c, eps, (E *)S, lds, Y, ldy, scales};
 }
 
 template <typename E, typename O, bool GATED> dyra_status run(const dyra::LinearArgs<E, O> &a, hipStream_t st) {
@@ -107,6 +163,101 @@ dyra_status dyra_gated(const void *X, int64_t ldx, const void *Wg, const void *W
     if (dtype == DYRA_F32)
         return run_linear<float, float, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
     return run_linear<bf16, bf16, true>(X, ldx, Wg, Wu, ldw, N, c1, c2, bias_g, bias_u, act, nullptr, 0, H, ldh, stream);
+}
+
+dyra_status dyra_norm(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, const void *residual, int64_t ldr,
+                      const void *weight, float eps, void *S, int64_t lds, void *Y, int64_t ldy, void *stream) {
+    bool empty;
+    const dyra_status s = check_norm(X, ldx, N, c, dtype, residual, ldr, weight, eps, S, lds, Y, ldy, &empty);
+    if (s != DYRA_OK || empty) return s;
+    if (!aligned(Y, size_of(dtype))) return DYRA_ERR_ALIGN;
+    if (among(Y, {residual, weight, S}) || other_rows(Y, ldy, N, X, ldx) || among(S, {weight})) return DYRA_ERR_ARG;
+    if (other_rows(S, lds, N, residual, ldr) || among(S, {X})) return DYRA_ERR_ARG;
+    auto go = [&](auto e) {
+        typedef decltype(e) E;
+        return hip_status(dyra::launch_norm<E>(row_args<E>(X, ldx, N, c, residual, ldr, weight, eps, S, lds, Y, ldy, nullptr), (hipStream_t)stream));
+    };
+    return dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
+}
+
+dyra_status dyra_norm_quantize(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, const void *residual,
+                               int64_t ldr, const void *weight, float eps, void *S, int64_t lds, int8_t *Q, int64_t ldq,
+                               float *scales, void *stream) {
+    bool empty;
+    const dyra_status s = check_norm(X, ldx, N, c, dtype, residual, ldr, weight, eps, S, lds, Q, ldq, &empty);
+    if (s != DYRA_OK || empty) return s;
+    if (!scales) return DYRA_ERR_ARG;
+    if (!aligned(scales, 4)) return DYRA_ERR_ALIGN;
+    if (among(Q, {X, residual, weight, S, scales}) || among(scales, {X, residual, weight, S})) return DYRA_ERR_ARG;
+    if (other_rows(S, lds, N, residual, ldr) || among(S, {X, weight})) return DYRA_ERR_ARG;
+    auto go = [&](auto e) {
+        typedef decltype(e) E;
+        return hip_status(dyra::launch_norm_quantize<E>(row_args<E>(X, ldx, N, c, residual, ldr, weight, eps, S, lds, Q, ldq, scales), (hipStream_t)stream));
+    };
+    return dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
+}
+
+dyra_status dyra_quantize(const void *X, int64_t ldx, int64_t N, int64_t c, dyra_dtype dtype, int8_t *Q, int64_t ldq,
+                          float *scales, void *stream) {
+    bool empty;
+    const dyra_status s = check_rows(X, ldx, N, c, dtype, Q, ldq, &empty);
+    if (s != DYRA_OK || empty) return s;
+    if (!scales) return DYRA_ERR_ARG;
+    if (!aligned(X, size_of(dtype)) || !aligned(scales, 4)) return DYRA_ERR_ALIGN;
+    if (among(Q, {X, scales}) || among(scales, {X})) return DYRA_ERR_ARG;
+    auto go = [&](auto e) {
+        typedef decltype(e) E;
+        return hip_status(dyra::launch_quantize<E>(row_args<E>(X, ldx, N, c, nullptr, 0, nullptr, 0.f, nullptr, 0, Q, ldq, scales), (hipStream_t)stream));
+    };
+    return dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
+}
+
+dyra_status dyra_dequantize(const int8_t *Q, int64_t ldq, const float *scales, int64_t N, int64_t c, dyra_dtype dtype, void *X,
+                            int64_t ldx, void *stream) {
+    bool empty;
+    const dyra_status s = check_rows(Q, ldq, N, c, dtype, X, ldx, &empty);
+    if (s != DYRA_OK || empty) return s;
+    if (!scales) return DYRA_ERR_ARG;
+    if (!aligned(X, size_of(dtype)) || !aligned(scales, 4)) return DYRA_ERR_ALIGN;
+    if (among(X, {Q, scales})) return DYRA_ERR_ARG;
+    hipStream_t st = (hipStream_t)stream;
+    return hip_status(dtype == DYRA_BF16 ? dyra::launch_dequantize<bf16>(Q, ldq, scales, N, c, (bf16 *)X, ldx, st)
+                                         : dyra::launch_dequantize<float>(Q, ldq, scales, N, c, (float *)X, ldx, st));
+}
+
+dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wt, int64_t ldw,
+                                  const float *w_scales, int64_t N, int64_t c1, int64_t c2, const void *bias, dyra_act act,
+                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *stream) {
+    bool empty;
+    const dyra_status s = check_quantized(X, ldx, x_scales, Wt, Wt, ldw, w_scales, w_scales, N, c1, c2, bias, nullptr, act, Y, ldy, out_dtype, &empty);
+    if (s != DYRA_OK) return s;
+    if (residual && ldr != 0 && ldr < c2) return DYRA_ERR_ARG;
+    if (empty) return DYRA_OK;
+    if (!aligned(residual, size_of(out_dtype))) return DYRA_ERR_ALIGN;
+    if (among(Y, {X, x_scales, Wt, w_scales, bias}) || other_rows(Y, ldy, N, residual, ldr)) return DYRA_ERR_ARG;
+    if (!residual) ldr = 0;
+    auto go = [&](auto o) {
+        typedef decltype(o) O;
+        return run<i8, O, false>({X, ldx, Wt, nullptr, ldw, N, c2, c1, (const O *)bias, nullptr, (const O *)residual, ldr, (O *)Y, ldy, (int)act,
+                                  {x_scales, w_scales, nullptr}}, (hipStream_t)stream);
+    };
+    return out_dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
+}
+
+dyra_status dyra_gated_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wg, const float *g_scales,
+                                 const int8_t *Wu, const float *u_scales, int64_t ldw, int64_t N, int64_t c1, int64_t c2,
+                                 const void *bias_g, const void *bias_u, dyra_act act, dyra_dtype out_dtype, void *H,
+                                 int64_t ldh, void *stream) {
+    bool empty;
+    const dyra_status s = check_quantized(X, ldx, x_scales, Wg, Wu, ldw, g_scales, u_scales, N, c1, c2, bias_g, bias_u, act, H, ldh, out_dtype, &empty);
+    if (s != DYRA_OK || empty) return s;
+    if (among(H, {X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u})) return DYRA_ERR_ARG;
+    auto go = [&](auto o) {
+        typedef decltype(o) O;
+        return run<i8, O, true>({X, ldx, Wg, Wu, ldw, N, c2, c1, (const O *)bias_g, (const O *)bias_u, nullptr, 0, (O *)H, ldh, (int)act,
+                                 {x_scales, g_scales, u_scales}}, (hipStream_t)stream);
+    };
+    return out_dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
 }
 
 dyra_status dyra_route(const void *logits, int64_t ld, int64_t T, int32_t experts, int32_t topk, dyra_dtype dtype,

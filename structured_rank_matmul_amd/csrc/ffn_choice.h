@@ -1,7 +1,7 @@
 // Which kernel a feed-forward call runs, from its sizes alone: host code without
 // HIP, so that a test on the CPU can list the variants and see that each is
 // tested.  Sizes are of the argument checks' ranges; `elem` is the bytes of an
-// operand's element (2 or 4).
+// operand's element (1, 2 or 4).
 #pragma once
 
 #include <stdint.h>
@@ -13,7 +13,7 @@ namespace dyra {
 
 // ------------------------------------------------------------------ linear layer, gated pair
 
-// Up to this many tokens the weights are streamed (skinny.hip).
+// Up to this many tokens the weights are streamed (skinny_linear.h).
 constexpr int64_t kSkinnyTokens = 32;
 // Whether X is streamed and the weights' rows take the tokens' part (launch_narrow):
 // few features, one unit of 16 tokens a CU; float32, where the tiles are bound by their
@@ -69,10 +69,10 @@ inline Tile pick_tile(int elem, bool gated, int64_t M, int64_t N, int64_t row_by
     const double rows = (double)N * (gated ? 2 : 1), slabs = std::ceil((double)row_bytes / 128.0);
     Tile best = T32x64;
     double cost = 1e300;
-    for (int i = T32x64; i <= (elem == 2 ? T256x256 : T128x128); ++i) {
+    for (int i = T32x64; i <= (elem != 4 ? T256x256 : T128x128); ++i) {
         const TileCost &t = kTiles[i];
         const double rounds = std::ceil(std::ceil((double)M / t.bm) * std::ceil(rows / t.bn) / 256.0);
-        const double c = rounds * (slabs * (elem == 2 ? t.slab : t.slab_f32) + t.once);
+        const double c = rounds * (slabs * (elem != 4 ? t.slab : t.slab_f32) + t.once);
         if (c < cost) {
             cost = c;
             best = (Tile)i;

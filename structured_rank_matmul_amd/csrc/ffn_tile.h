@@ -28,6 +28,24 @@ __device__ __forceinline__ f32x4 mma32(f32x4 acc, f32x8 a, f32x8 b) {
     for (int t = 0; t < 8; ++t) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[t], b[t], acc, 0, 0, 0);
     return acc;
 }
+// 64 deep: the fragments are 16 bytes of 8-bit integers, the sums exact.
+__device__ __forceinline__ i32x4 mma32(i32x4 acc, i32x4 a, i32x4 b) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+}
+template <> struct Frag<i8> { typedef i32x4 type; };
+
+// Sums of products, and how many steps the MFMA blocks take over 128 bytes of K.
+template <typename E> struct Sums { typedef f32x4 type; };
+template <> struct Sums<i8> { typedef i32x4 type; };
+template <typename E> constexpr int slab_steps() { return sizeof(E) == 4 ? 1 : 2; }
+
+// A result before its activation: a sum with its bias, or of 8-bit operands with its
+// scales.  The scales' product is taken first: it leaves float32's range only with the
+// result.
+__device__ __forceinline__ float biased(float sum, float, float, float b) { return sum + b; }
+__device__ __forceinline__ float biased(int sum, float sx, float sw, float b) {
+    return __builtin_fmaf((float)sum, sx * sw, b);
+}
 
 // A buffer resource over `bytes` (at most 2 GiB) from `p` on; loads past them, at
 // kOutside among them, give 0.

@@ -51,9 +51,11 @@ __device__ __forceinline__ int fresh_lane() {
     return l;
 }
 
-template <typename O, bool GATED, int TB>
-__global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> a, int tiles_m, int tiles_n,
+template <typename E, typename O, bool GATED, int TB>
+__global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, int tiles_m, int tiles_n,
                                                             int per_xcd) {
+    typedef typename Frag<E>::type F;
+    typedef typename Sums<E>::type Acc;
     constexpr int BM = 32 * TB, BF = GATED ? 128 : 256;
     constexpr int STAGE = 32768, WOFF = 65536;  // two buffers of 256 token rows of 128 bytes, two of 256 weight rows
     // 16-byte stores of a wavefront's epilogue
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         if constexpr (GATED) wbuf1 = panel(a.W1 + col0 * a.ldw);
         const int tmax = (int)min(a.M - 1 - row0, (int64_t)BM - 1), fmax = (int)min(a.N - 1 - col0, (int64_t)BF - 1);
         const int lr = fresh_lane() >> 3;
-        const uint32_t xld = (uint32_t)(2 * a.ldx), wld = (uint32_t)(2 * a.ldw);
+        const uint32_t xld = (uint32_t)((int64_t)sizeof(E) * a.ldx), wld = (uint32_t)((int64_t)sizeof(E) * a.ldw);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -105,9 +107,10 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
                 woff[h][q] = (uint32_t)min(f, fmax) * wld + wchunk;
             }
     };
-    const int slabs = 2 * (int)((a.K + 127) / 128);
+    constexpr int PAIR = 256 / (int)sizeof(E);  // elements of two slabs of a row
+    const int slabs = 2 * (int)((a.K + PAIR - 1) / PAIR);
     // the slab that the copies are at: its bytes left in a row, its buffer
-    int cs = 0, left = (int)min((int64_t)INT32_MAX, 2 * a.K);
+    int cs = 0, left = (int)min((int64_t)INT32_MAX, (int64_t)sizeof(E) * a.K);
     const int row_bytes = left;
     auto copy_x = [&](int h, int buf) __attribute__((always_inline)) {
         char *dst = smem + buf * STAGE + (64 * h + 8 * wave) * 128;
@@ -139,9 +142,9 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         }
     };
 
-    f32x4 acc[2][2][4][2];  // [token half][weight half][token block][weight block]
-    bf16x8 fx[2][4];        // [32-deep step][token block]
-    bf16x8 fw[3][2][2];     // [slot][step][weight block]
+    Acc acc[2][2][4][2];  // [token half][weight half][token block][weight block]
+    F fx[2][4];           // [step][token block]
+    F fw[3][2][2];        // [slot][step][weight block]
 
     const int swx = (i16 >> 1) & 7, sww = ((i16 >> 1) & 1) | ((i16 >> 2) << 1);
     const char *const px = smem + (128 * wm + i16) * 128;
@@ -152,7 +155,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < (h == 0 ? 4 : TB - 4); ++i)
-                fx[k][i] = *reinterpret_cast<const bf16x8 *>(p + 16 * i * 128 + (((4 * k + g) ^ swx) << 4));
+                fx[k][i] = *reinterpret_cast<const F *>(p + 16 * i * 128 + (((4 * k + g) ^ swx) << 4));
     };
     auto read_w = [&](int h, int buf, int slot) __attribute__((always_inline)) {
         const char *p = pw + buf * STAGE + 32 * h * 128;
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                fw[slot][k][j] = *reinterpret_cast<const bf16x8 *>(p + 4 * j * 128 + (((4 * k + g) ^ sww) << 4));
+                fw[slot][k][j] = *reinterpret_cast<const F *>(p + 4 * j * 128 + (((4 * k + g) ^ sww) << 4));
     };
     // 32 MFMAs: token half hx with both weight halves
     auto products = [&](int hx, int slot_a, int slot_b) __attribute__((always_inline)) {
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
     for (;;) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            f32x4 z = {};
+            Acc z = {};
             asm volatile("" : "+v"(z));  // plain zeroed registers: no first iteration of its own
             acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] = z;
         }
@@ -249,6 +252,14 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
         for (int hw = 0; hw < HW; ++hw)
             if (a.b0) load_row(a.b0 + c + 32 * hw, b0[hw], whole ? 8 : (int)(a.N - c) - 32 * hw);
         if (GATED && a.b1) load_row(a.b1 + c, b1, whole ? 8 : (int)(a.N - c));
+        float sx[TB] = {}, s0[HW][8] = {}, s1[8] = {};  // scales of 8-bit operands
+        if constexpr (sizeof(E) == 1) {
+#pragma unroll
+            for (int i = 0; i < TB; ++i) sx[i] = a.scale.x[min(row0 + 16 * (TB * wm + i) + ei, a.M - 1)];
+#pragma unroll
+            for (int hw = 0; hw < HW; ++hw) load_row(a.scale.w0 + c + 32 * hw, s0[hw], whole ? 8 : (int)(a.N - c) - 32 * hw);
+            if constexpr (GATED) load_row(a.scale.w1 + c, s1, whole ? 8 : (int)(a.N - c));
+        }
         // ACT below 0: of the call, with guards
         auto finish = [&](auto act, auto residual) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
@@ -275,11 +286,11 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
                         const int have = ACT >= 0 ? 8 : (int)max((int64_t)0, min((int64_t)8, a.N - c - 32 * hw));
                         float v[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] = acc[i >> 2][hw][i & 3][q >> 2][q & 3] + b0[hw][q];
+                        for (int q = 0; q < 8; ++q) v[q] = biased(acc[i >> 2][hw][i & 3][q >> 2][q & 3], sx[i], s0[hw][q], b0[hw][q]);
                         activate<sizeof(O) == 4>(v, ACT >= 0 ? ACT : a.act);
                         if constexpr (GATED) {
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) v[q] *= acc[i >> 2][1][i & 3][q >> 2][q & 3] + b1[q];
+                            for (int q = 0; q < 8; ++q) v[q] *= biased(acc[i >> 2][1][i & 3][q >> 2][q & 3], sx[i], s1[q], b1[q]);
                         }
                         if constexpr (RESIDUAL && ACT >= 0) r[i - i0][hw].add_to(v);
                         else if constexpr (RESIDUAL) add_row(v, a.R + t * a.ldr + c + 32 * hw, have);
@@ -309,14 +320,14 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<bf16, O> 
     wait_vmcnt<0>();  // no copy may land in LDS after the workgroup has given it back
 }
 
-template <typename O, bool GATED, int TB> hipError_t launch_big(const LinearArgs<bf16, O> &a, hipStream_t st) {
+template <typename E, typename O, bool GATED, int TB> hipError_t launch_big(const LinearArgs<E, O> &a, hipStream_t st) {
     const int64_t tiles_m = (a.M + 32 * TB - 1) / (32 * TB), tiles_n = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
     const int64_t ntiles = tiles_m * tiles_n;
     if (ntiles > (int64_t)1 << 24) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
     // one workgroup per CU: 32 on each XCD
     const int64_t slots = per_xcd < 32 ? per_xcd : 32;
-    hipLaunchKernelGGL((linear_big_kernel<O, GATED, TB>), dim3((unsigned)(8 * slots)), dim3(512), 0, st, a, (int)tiles_m,
+    hipLaunchKernelGGL((linear_big_kernel<E, O, GATED, TB>), dim3((unsigned)(8 * slots)), dim3(512), 0, st, a, (int)tiles_m,
                        (int)tiles_n, (int)per_xcd);
     return hipGetLastError();
 }

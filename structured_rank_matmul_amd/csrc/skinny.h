@@ -1,4 +1,4 @@
-// Streaming products for few tokens (skinny.hip, moe.hip): each wavefront runs
+// Streaming products for few tokens (skinny_linear.h, moe.hip): each wavefront runs
 // its own stream of slabs from global memory through a ring in LDS, with no
 // barrier, so that the loads of the slabs ahead are always in flight.
 //
@@ -36,12 +36,15 @@ struct SlabRows {
     uint32_t off[2];
 };
 
-// Fragments of one slab: 128 bytes of K are STEPS steps of 32 elements.
+// Fragments of one slab: STEPS steps over 128 bytes of K.
 template <typename E> struct SlabFrag {
-    static constexpr int STEPS = 128 / (32 * (int)sizeof(E));
+    static constexpr int STEPS = slab_steps<E>();
     typename Frag<E>::type f[STEPS];
 };
 __device__ __forceinline__ f32x4 slab_product(f32x4 acc, const SlabFrag<bf16> &w, const SlabFrag<bf16> &x) {
+    return mma32(mma32(acc, w.f[0], x.f[0]), w.f[1], x.f[1]);
+}
+__device__ __forceinline__ i32x4 slab_product(i32x4 acc, const SlabFrag<i8> &w, const SlabFrag<i8> &x) {
     return mma32(mma32(acc, w.f[0], x.f[0]), w.f[1], x.f[1]);
 }
 __device__ __forceinline__ f32x4 slab_product(f32x4 acc, const SlabFrag<float> &w, const SlabFrag<float> &x) {
@@ -52,9 +55,9 @@ template <typename E, int ROWS> __device__ __forceinline__ SlabFrag<E> slab_read
     const int lane = threadIdx.x & 63, r16 = lane & (ROWS - 1), g = lane >> 4, sw = r16 & 7;
     const char *p = slab + r16 * 128;
     SlabFrag<E> r;
-    if constexpr (sizeof(E) == 2) {
+    if constexpr (sizeof(E) != 4) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) r.f[h] = *reinterpret_cast<const bf16x8 *>(p + (((4 * h + g) ^ sw) << 4));
+        for (int h = 0; h < 2; ++h) r.f[h] = *reinterpret_cast<const typename Frag<E>::type *>(p + (((4 * h + g) ^ sw) << 4));
     } else {
         const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + ((g ^ sw) << 4));
         const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + (((4 + g) ^ sw) << 4));
@@ -72,9 +75,9 @@ template <typename E> __device__ __forceinline__ SlabFrag<E> slab_load(__amdgpu_
     auto chunk = [&](uint32_t c) -> u32x4 {
         return __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(16 * c) < left ? row + 16 * c : kOutside, (int)k, 0);
     };
-    if constexpr (sizeof(E) == 2) {
+    if constexpr (sizeof(E) != 4) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) r.f[h] = __builtin_bit_cast(bf16x8, chunk(4 * h + g));
+        for (int h = 0; h < 2; ++h) r.f[h] = __builtin_bit_cast(typename Frag<E>::type, chunk(4 * h + g));
     } else {
         const f32x4 lo = __builtin_bit_cast(f32x4, chunk(g)), hi = __builtin_bit_cast(f32x4, chunk(4 + g));
         r.f[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -158,11 +161,12 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kBlockSums = 256;  // floats of a block's sums: token, then row
-// The sum over the wavefronts of row r of a block's token i.
-__device__ __forceinline__ float joined(const float *block, int i, int r) {
-    float z = 0.f;
+// The sum over the wavefronts of row r of a block's token i; S float, or int for
+// 8-bit operands, whose sums lie in the same places.
+template <typename S = float> __device__ __forceinline__ S joined(const float *block, int i, int r) {
+    S z = 0;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) z += block[v * kBlockSums + i * 16 + r];
+    for (int v = 0; v < kWaves; ++v) z += reinterpret_cast<const S *>(block)[v * kBlockSums + i * 16 + r];
     return z;
 }
 // One variable, so that the compiler sees no separate objects whose accesses it
@@ -229,7 +233,8 @@ __device__ __forceinline__ void stream_products(const Position &start, int row_b
             stale = parts || at.new_tokens();
         }
         const bool two = TB == 2 && at.blocks() == 2;
-        f32x4 acc[TB] = {};
+        typedef typename Sums<E>::type Acc;
+        Acc acc[TB] = {};
         for (int base = s0; base < s1; base += SLABS) {
             if (stale) {
                 load_tokens(at, base);
@@ -251,8 +256,8 @@ __device__ __forceinline__ void stream_products(const Position &start, int row_b
         was_two = two;
         set = two ? 0 : set ^ 1;
         float *mine = &lds.sums[set][wave][(lane & 15) * 16 + 4 * (lane >> 4)];
-        *reinterpret_cast<f32x4 *>(mine) = acc[0];
-        if (two) *reinterpret_cast<f32x4 *>(mine + kWaves * kBlockSums) = acc[TB - 1];
+        *reinterpret_cast<Acc *>(mine) = acc[0];
+        if (two) *reinterpret_cast<Acc *>(mine + kWaves * kBlockSums) = acc[TB - 1];
         __syncthreads();
         at.finish(&lds.sums[set][0][0], (tid - begin) & (kThreads - 1));
         begin += Position::kFinishers;  // other wavefronts finish the next one

@@ -29,6 +29,7 @@ EXPORTED = (
     "dyra_forward_timed", "dyra_stage_name", "dyra_prepare_blast", "dyra_factorize_blast_host",
     "dyra_forward_noalloc", "dyra_noalloc_scratch_bytes",
     "dyra_linear", "dyra_gated", "dyra_route", "dyra_moe", "dyra_moe_workspace_bytes",
+    "dyra_norm", "dyra_norm_quantize", "dyra_quantize", "dyra_dequantize", "dyra_linear_quantized", "dyra_gated_quantized",
 )
 
 
@@ -100,6 +101,18 @@ def load() -> ctypes.CDLL:
     L.dyra_moe.restype = ctypes.c_int
     L.dyra_moe_workspace_bytes.argtypes = [i64, i32, i64, en]
     L.dyra_moe_workspace_bytes.restype = ctypes.c_size_t
+    L.dyra_norm.argtypes = [vp, i64, i64, i64, en, vp, i64, vp, f32, vp, i64, vp, i64, vp]
+    L.dyra_norm.restype = ctypes.c_int
+    L.dyra_norm_quantize.argtypes = [vp, i64, i64, i64, en, vp, i64, vp, f32, vp, i64, vp, i64, vp, vp]
+    L.dyra_norm_quantize.restype = ctypes.c_int
+    L.dyra_quantize.argtypes = [vp, i64, i64, i64, en, vp, i64, vp, vp]
+    L.dyra_quantize.restype = ctypes.c_int
+    L.dyra_dequantize.argtypes = [vp, i64, vp, i64, i64, en, vp, i64, vp]
+    L.dyra_dequantize.restype = ctypes.c_int
+    L.dyra_linear_quantized.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, en, vp, i64, en, vp, i64, vp]
+    L.dyra_linear_quantized.restype = ctypes.c_int
+    L.dyra_gated_quantized.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, en, en, vp, i64, vp]
+    L.dyra_gated_quantized.restype = ctypes.c_int
     L.dyra_stage_name.argtypes = [vp, i64, i32]
     L.dyra_stage_name.restype = ctypes.c_char_p
     _lib = L
@@ -552,6 +565,187 @@ def dyra_gated(X, Wg, Wu, bias_g=None, bias_u=None, act: str = "silu", H=None, s
                                          code, H.data_ptr(), ldh, st)
     if status != 0:
         raise DyraError(status, "dyra_gated")
+    return H
+
+
+def _types():
+    """(torch.int8, torch.float32, torch.bfloat16)"""
+    global _torch_types
+    if _torch_types is None:
+        import torch
+        _torch_types = (torch.int8, torch.float32, torch.bfloat16)
+    return _torch_types
+
+
+_torch_types = None
+
+
+def _norm_inputs(X, N, c, dev, weight, residual, S, stream):
+    """(weight, residual, its row stride, S tensor, its address, its row stride) of the norms."""
+    t = X.dtype
+    w = None if weight is None else _whole(weight, "weight", dev, (c,), t)
+    if residual is None:
+        if S is not None:
+            raise ValueError("S is written for a residual only")
+        return w, None, 0, None, None, 0
+    r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c, t, True)
+    if S is None:
+        S, lds = _new((N, c), t, X, stream), c
+    else:
+        lds = _matrix(S, "S", dev, N, c, t)
+    return w, r, ldr, S, S.data_ptr(), lds
+
+
+def dyra_norm(X, weight=None, eps: float = 1e-6, residual=None, S=None, Y=None, stream=None):
+    """Y = Z / sqrt(mean(Z^2) + eps) * weight of every row of Z = X + residual; X [N, c].  With a residual returns
+    (Y, S), S = Z rounded: the residual stream for what follows (S may be the residual itself, Y may be X)."""
+    N, c, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_norm, X, weight, eps, residual, S, Y, stream)
+    t = X.dtype
+    code = _codes[t]
+    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, dev, weight, residual, S, stream)
+    if Y is None:
+        Y, ldy = _new((N, c), t, X, stream), c
+    else:
+        ldy = _matrix(Y, "Y", dev, N, c, t)
+    status = (_lib or load()).dyra_norm(X.data_ptr(), ldx, N, c, code, r, ldr, w, eps, s, lds, Y.data_ptr(), ldy, st)
+    if status != 0:
+        raise DyraError(status, "dyra_norm")
+    return Y if S is None else (Y, S)
+
+
+def _eight_bits(X, N, c, dev, Q, scales, stream):
+    """(Q, its row stride, scales) to be written."""
+    i8, f32, _ = _types()
+    if Q is None:
+        Q, ldq = _new((N, c), i8, X, stream), c
+    else:
+        ldq = _matrix(Q, "Q", dev, N, c, i8)
+    if scales is None:
+        scales = _new((N,), f32, X, stream)
+    else:
+        _whole(scales, "scales", dev, (N,), f32)
+    return Q, ldq, scales
+
+
+def dyra_norm_quantize(X, weight=None, eps: float = 1e-6, residual=None, S=None, Q=None, scales=None, stream=None):
+    """dyra_norm with its result in 8 bits, as dyra_quantize gives it: (Q, scales), with a residual (Q, scales, S)."""
+    N, c, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_norm_quantize, X, weight, eps, residual, S, Q, scales, stream)
+    code = _codes[X.dtype]
+    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, dev, weight, residual, S, stream)
+    Q, ldq, scales = _eight_bits(X, N, c, dev, Q, scales, stream)
+    status = (_lib or load()).dyra_norm_quantize(X.data_ptr(), ldx, N, c, code, r, ldr, w, eps, s, lds, Q.data_ptr(), ldq,
+                                                 scales.data_ptr(), st)
+    if status != 0:
+        raise DyraError(status, "dyra_norm_quantize")
+    return (Q, scales) if S is None else (Q, scales, S)
+
+
+def dyra_quantize(X, Q=None, scales=None, stream=None):
+    """(Q int8 [N, c], scales float32 [N]) of X [N, c]: every row's largest magnitude over 127, and the whole numbers
+    nearest to its values over that.  Of a weight [c2, c1]: a scale for each output feature."""
+    N, c, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_quantize, X, Q, scales, stream)
+    code = _codes[X.dtype]
+    Q, ldq, scales = _eight_bits(X, N, c, dev, Q, scales, stream)
+    status = (_lib or load()).dyra_quantize(X.data_ptr(), ldx, N, c, code, Q.data_ptr(), ldq, scales.data_ptr(), st)
+    if status != 0:
+        raise DyraError(status, "dyra_quantize")
+    return Q, scales
+
+
+def dyra_dequantize(Q, scales, out_dtype=None, X=None, stream=None):
+    """X = Q * scales, row by row, in out_dtype (bfloat16 by default)."""
+    N, c, ldq, dev = _input(Q, "Q")
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_dequantize, Q, scales, out_dtype, X, stream)
+    i8, f32, bf16 = _types()
+    if Q.dtype != i8:
+        raise ValueError(f"Q must be int8, got {Q.dtype}")
+    s = _whole(scales, "scales", dev, (N,), f32)
+    out = bf16 if out_dtype is None else out_dtype
+    code = _codes[out]
+    if X is None:
+        X, ldx = _new((N, c), out, Q, stream), c
+    else:
+        ldx = _matrix(X, "X", dev, N, c, out)
+    status = (_lib or load()).dyra_dequantize(Q.data_ptr(), ldq, s, N, c, code, X.data_ptr(), ldx, st)
+    if status != 0:
+        raise DyraError(status, "dyra_dequantize")
+    return X
+
+
+def dyra_linear_quantized(X, x_scales, Wt, w_scales, bias=None, act: str = "none", residual=None, out_dtype=None, Y=None,
+                          stream=None):
+    """dyra_linear on 8-bit integers: X int8 [N, c1] with a scale for each token, Wt int8 [c2, c1] with a scale for each
+    feature (both float32); bias, residual and Y in out_dtype (bfloat16 by default)."""
+    N, c1, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_linear_quantized, X, x_scales, Wt, w_scales, bias, act, residual, out_dtype, Y, stream)
+    i8, f32, bf16 = _types()
+    if X.dtype != i8:
+        raise ValueError(f"X must be int8, got {X.dtype}")
+    c2 = Wt.shape[0]
+    out = bf16 if out_dtype is None else out_dtype
+    code = _codes[out]
+    ldw = _matrix(Wt, "Wt", dev, c2, c1, i8)
+    sx, sw = _whole(x_scales, "x_scales", dev, (N,), f32), _whole(w_scales, "w_scales", dev, (c2,), f32)
+    b = None if bias is None else _whole(bias, "bias", dev, (c2,), out)
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c2, out, True)
+    acode = _ACTS[act]
+    if Y is None:
+        Y, ldy = _new((N, c2), out, X, stream), c2
+    else:
+        ldy = _matrix(Y, "Y", dev, N, c2, out)
+    status = (_lib or load()).dyra_linear_quantized(X.data_ptr(), ldx, sx, Wt.data_ptr(), ldw, sw, N, c1, c2, b, acode, r, ldr,
+                                                    code, Y.data_ptr(), ldy, st)
+    if status != 0:
+        raise DyraError(status, "dyra_linear_quantized")
+    return Y
+
+
+def dyra_gated_quantized(X, x_scales, Wg, g_scales, Wu, u_scales, bias_g=None, bias_u=None, act: str = "silu",
+                         out_dtype=None, H=None, stream=None):
+    """dyra_gated on 8-bit integers: Wg and Wu int8 [c2, c1] with one row stride and their scales for each feature; biases
+    and H in out_dtype (bfloat16 by default)."""
+    N, c1, ldx, dev = _input(X)
+    st = _stream_on(dev, stream)
+    if st is None:
+        return _with_device(dev, dyra_gated_quantized, X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u, act, out_dtype,
+                            H, stream)
+    i8, f32, bf16 = _types()
+    if X.dtype != i8:
+        raise ValueError(f"X must be int8, got {X.dtype}")
+    c2 = Wg.shape[0]
+    out = bf16 if out_dtype is None else out_dtype
+    code = _codes[out]
+    ldw = _matrix(Wg, "Wg", dev, c2, c1, i8)
+    if _matrix(Wu, "Wu", dev, c2, c1, i8) != ldw:
+        raise ValueError("Wg and Wu must have one row stride")
+    sx = _whole(x_scales, "x_scales", dev, (N,), f32)
+    sg, su = _whole(g_scales, "g_scales", dev, (c2,), f32), _whole(u_scales, "u_scales", dev, (c2,), f32)
+    bg = None if bias_g is None else _whole(bias_g, "bias_g", dev, (c2,), out)
+    bu = None if bias_u is None else _whole(bias_u, "bias_u", dev, (c2,), out)
+    acode = _ACTS[act]
+    if H is None:
+        H, ldh = _new((N, c2), out, X, stream), c2
+    else:
+        ldh = _matrix(H, "H", dev, N, c2, out)
+    status = (_lib or load()).dyra_gated_quantized(X.data_ptr(), ldx, sx, Wg.data_ptr(), sg, Wu.data_ptr(), su, ldw, N, c1, c2,
+                                                   bg, bu, acode, code, H.data_ptr(), ldh, st)
+    if status != 0:
+        raise DyraError(status, "dyra_gated_quantized")
     return H
 
 

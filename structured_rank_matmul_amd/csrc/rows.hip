@@ -20,7 +20,6 @@ namespace dyra {
 
 namespace {
 
-constexpr int kRowThreads = 256;
 constexpr float kLeastTop = 127.f * FLT_MIN;
 
 // What a row's threads find together: the sum of squares, and the largest magnitude as
@@ -29,80 +28,266 @@ struct RowStats {
     float sum;
     unsigned top;
 };
-__device__ __forceinline__ RowStats joined_row(RowStats v) {
-    __shared__ float sums[kRowThreads / 64];
-    __shared__ unsigned tops[kRowThreads / 64];
+// Joined over the THREADS of a row: neighbouring lanes of one wavefront, or a workgroup's
+// wavefronts, which all call it.
+template <int THREADS> __device__ __forceinline__ RowStats joined_row(RowStats v) {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
+    for (int d = (THREADS < 64 ? THREADS : 64) / 2; d > 0; d >>= 1) {
         v.sum += __shfl_xor(v.sum, d);
         v.top = max(v.top, (unsigned)__shfl_xor((int)v.top, d));
     }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-        sums[threadIdx.x >> 6] = v.sum;
-        tops[threadIdx.x >> 6] = v.top;
-    }
-    __syncthreads();
-    v = {0.f, 0u};
+    if constexpr (THREADS > 64) {
+        constexpr int W = THREADS / 64;
+        __shared__ float sums[W];
+        __shared__ unsigned tops[W];
+        __syncthreads();  // the last ones have been read
+        if ((threadIdx.x & 63) == 0) {
+            sums[threadIdx.x >> 6] = v.sum;
+            tops[threadIdx.x >> 6] = v.top;
+        }
+        __syncthreads();
+        v = {0.f, 0u};
 #pragma unroll
-    for (int i = 0; i < kRowThreads / 64; ++i) {
-        v.sum += sums[i];
-        v.top = max(v.top, tops[i]);
+        for (int i = 0; i < W; ++i) {
+            v.sum += sums[i];
+            v.top = max(v.top, tops[i]);
+        }
     }
     return v;
 }
 
-// One workgroup a row, which is read twice.
-template <typename E, bool NORM, bool EIGHT> __global__ __launch_bounds__(kRowThreads) void rows_kernel(RowArgs<E> a) {
-    const int64_t row = blockIdx.x;
-    const E *x = a.X + row * a.ldx, *r = a.R ? a.R + row * a.ldr : nullptr;
-    auto value = [&](int64_t j) { return to_f32(x[j]) + (r ? to_f32(r[j]) : 0.f); };
-    auto weight = [&](int64_t j) { return a.W ? to_f32(a.W[j]) : 1.f; };
+// V elements as they lie in memory (16 bytes), any alignment of their type.
+template <typename E> struct Chunk {
+    static constexpr int V = 16 / (int)sizeof(E);
+    union {
+        u32x4 u;
+        E e[V];
+    };
+    __device__ __forceinline__ void load(const E *p) { u = *reinterpret_cast<const u32x4_any *>(p); }
+    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<u32x4_any *>(p) = u; }
+};
+
+// The whole number nearest to y * steps (|y * steps| < 2^21) in the low bits: added to
+// 1.5 2^23, a float32 whose last place is 1.
+__device__ __forceinline__ unsigned nearest(float y, float steps) {
+    return __float_as_uint(__builtin_fmaf(y, steps, 12582912.f));
+}
+// The low bytes of four.
+__device__ __forceinline__ unsigned bytes4(unsigned a, unsigned b, unsigned c, unsigned d) {
+    const unsigned lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+    return lo | hi << 16;
+}
+template <int V> __device__ __forceinline__ void store_bytes(i8 *p, const unsigned (&q)[V]) {
+    typedef unsigned u32_any __attribute__((aligned(1)));
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 u32x2_any __attribute__((aligned(1)));
+    if constexpr (V == 4) *reinterpret_cast<u32_any *>(p) = bytes4(q[0], q[1], q[2], q[3]);
+    else *reinterpret_cast<u32x2_any *>(p) = u32x2{bytes4(q[0], q[1], q[2], q[3]), bytes4(q[4], q[5], q[6], q[7])};
+}
+
+// Threads of a workgroup: rows within a wavefront share one, longer rows have their own.
+constexpr int rows_threads(int row) { return row <= 64 ? 256 : row; }
+
+// THREADS threads hold a row of up to THREADS * CHUNKS whole 16-byte chunks, and one
+// more element each of the rest: it is read once, all its loads in flight together.  Bound
+// by memory: 16384 x 4096 bf16 with residual 81.5 us to 8 bits (5.8 TB/s of read and
+// written bytes) and 95 to bf16 (5.7); quantisation 34 us (5.9), 16384 x 14336 128 (5.5).
+// One workgroup a row that was read twice, by elements: 255, 105 at 25728 x 1024 (39), 330.
+template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
+__global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> a) {
+    constexpr int V = Chunk<E>::V, ROWS = rows_threads(THREADS) / THREADS;
+    const int t = threadIdx.x % THREADS;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
+    if (ROWS > 1 && row >= a.N) return;  // all threads of a row, which wait for no others
+    const int c = (int)a.c, chunks = c / V, rest = chunks * V + t;
+    const bool last = rest < c;
+    const E *const x = a.X + row * a.ldx, *const r = NORM && a.R ? a.R + row * a.ldr : nullptr;
+
+    float z[CHUNKS][V], z1 = 0.f;
+    {
+        Chunk<E> xs[CHUNKS], rs[CHUNKS];
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            xs[i].u = rs[i].u = u32x4{};
+            const int k = t + i * THREADS;
+            if (k < chunks) {
+                xs[i].load(x + k * V);
+                if (r) rs[i].load(r + k * V);
+            }
+        }
+        if (last) z1 = to_f32(x[rest]) + (r ? to_f32(r[rest]) : 0.f);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (int q = 0; q < V; ++q) z[i][q] = to_f32(xs[i].e[q]) + (r ? to_f32(rs[i].e[q]) : 0.f);
+    }
+    if (NORM && a.S) {
+        E *const s = a.S + row * a.lds;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int k = t + i * THREADS;
+            if (k < chunks) {
+                Chunk<E> o;
+#pragma unroll
+                for (int q = 0; q < V; ++q) o.e[q] = to_elem<E>(z[i][q]);
+                o.store(s + k * V);
+            }
+        }
+        if (last) s[rest] = to_elem<E>(z1);
+    }
+
+    // The longest rows' weights are read again where they are used, the others held.
+    constexpr bool HELD = CHUNKS * V * THREADS < 65536;
+    Chunk<E> ws[HELD ? CHUNKS : 1];
+    float w1 = 1.f;
+    const bool weighted = NORM && a.W;
+    auto load_weights = [&](int i) __attribute__((always_inline)) {
+        Chunk<E> &w = ws[HELD ? i : 0];
+        w.u = u32x4{};
+        const int k = t + i * THREADS;
+        if (k < chunks) w.load(a.W + k * V);
+    };
+    if (weighted) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) load_weights(i);
+        }
+        if (last) w1 = to_f32(a.W[rest]);
+    }
+    // before the first use of a chunk's weights
+    auto weights = [&](int i) __attribute__((always_inline)) {
+        if (!HELD && weighted) {
+            asm volatile("" ::: "memory");
+            load_weights(i);
+        }
+    };
+    auto weight = [&](int i, int q) { return weighted ? to_f32(ws[HELD ? i : 0].e[q]) : 1.f; };
     auto stats = [&](float by) {
         RowStats v = {0.f, 0u};
-        for (int64_t j = threadIdx.x; j < a.c; j += kRowThreads) {
-            const float z = value(j) * by;
-            v.sum += z * z;
-            v.top = max(v.top, __float_as_uint(z * weight(j)) & 0x7fffffffu);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            if (EIGHT) weights(i);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float y = z[i][q] * by;
+                if (NORM) v.sum = __builtin_fmaf(y, y, v.sum);
+                if (EIGHT) v.top = max(v.top, __float_as_uint(y * weight(i, q)) & 0x7fffffffu);
+            }
         }
-        return joined_row(v);
+        if (NORM) v.sum = __builtin_fmaf(z1 * by, z1 * by, v.sum);
+        if (EIGHT) v.top = max(v.top, __float_as_uint(z1 * by * w1) & 0x7fffffffu);
+        return joined_row<THREADS>(v);
     };
     float by = 1.f, rho = 1.f;
-    RowStats v = stats(by);
+    RowStats v = stats(1.f);
     if constexpr (NORM) {
         if (!(v.sum < INFINITY)) {
             by = 0x1p-96f;
             v = stats(by);
         }
-        rho = 1.f / sqrtf(v.sum / (float)a.c + a.eps * (by * by));
+        rho = 1.f / sqrtf(v.sum / (float)c + a.eps * (by * by));
     }
-    const float top = fmaxf(__uint_as_float(v.top) * rho, kLeastTop);
-    const bool finite = v.top < 0x7f800000u && top < INFINITY;
-    if (EIGHT && threadIdx.x == 0) a.scales[row] = finite ? top / 127.f : NAN;
-    const float steps = 127.f / top;
-    for (int64_t j = threadIdx.x; j < a.c; j += kRowThreads) {
-        const float z = value(j);
-        if (NORM && a.S) a.S[row * a.lds + j] = to_elem<E>(z);
-        if constexpr (EIGHT) {
-            const float y = z * by * weight(j) * rho;
-            ((i8 *)a.Y)[row * a.ldy + j] = finite ? (i8)(int)rintf(y * steps) : 0;
-        } else {
-            ((E *)a.Y)[row * a.ldy + j] = to_elem<E>(z * by * rho * weight(j));
+    if constexpr (EIGHT) {
+        const float top = fmaxf(__uint_as_float(v.top) * rho, kLeastTop);
+        const bool finite = v.top < 0x7f800000u && top < INFINITY;
+        if (t == 0) a.scales[row] = finite ? top / 127.f : NAN;
+        const float steps = 127.f / top;
+        i8 *const y = (i8 *)a.Y + row * a.ldy;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int k = t + i * THREADS;
+            weights(i);
+            if (k < chunks) {
+                unsigned b[V];
+#pragma unroll
+                for (int q = 0; q < V; ++q) b[q] = finite ? nearest(z[i][q] * by * weight(i, q) * rho, steps) : 0u;
+                store_bytes<V>(y + k * V, b);
+            }
         }
+        if (last) y[rest] = (i8)(finite ? nearest(z1 * by * w1 * rho, steps) : 0u);
+    } else {
+        E *const y = (E *)a.Y + row * a.ldy;
+        const float by_rho = by * rho;  // of a row that is summed again, at least 2^-96 / (2^32 sqrt c)
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int k = t + i * THREADS;
+            weights(i);
+            if (k < chunks) {
+                Chunk<E> o;
+#pragma unroll
+                for (int q = 0; q < V; ++q) o.e[q] = to_elem<E>(z[i][q] * by_rho * weight(i, q));
+                o.store(y + k * V);
+            }
+        }
+        if (last) y[rest] = to_elem<E>(z1 * by_rho * w1);
     }
 }
 
-template <typename E>
-__global__ __launch_bounds__(kRowThreads) void dequantize_kernel(const i8 *Q, int64_t ldq, const float *scales, int64_t c,
-                                                                E *X, int64_t ldx) {
-    const int64_t row = blockIdx.x;
+// Back: 16 bytes of results a thread, THREADS threads to a piece of a row.
+template <typename E, int THREADS>
+__global__ __launch_bounds__(256) void dequantize_kernel(const i8 *Q, int64_t ldq, const float *scales, int64_t N, int c, E *X,
+                                                         int64_t ldx) {
+    constexpr int V = Chunk<E>::V, ROWS = 256 / THREADS;
+    typedef unsigned u32xn __attribute__((ext_vector_type(V / 4)));
+    typedef u32xn u32xn_any __attribute__((aligned(1)));
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
+    if (row >= N) return;
+    const int at = V * ((int)threadIdx.x % THREADS + (int)blockIdx.y * THREADS);
+    const i8 *const from = Q + row * ldq;
+    E *const to = X + row * ldx;
     const float s = scales[row];
-    for (int64_t j = threadIdx.x; j < c; j += kRowThreads) X[row * ldx + j] = to_elem<E>((float)Q[row * ldq + j] * s);
+    if (at + V <= c) {
+        union {
+            u32xn u;
+            i8 e[V];
+        } q;
+        q.u = *reinterpret_cast<const u32xn_any *>(from + at);
+        Chunk<E> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.e[j] = to_elem<E>((float)q.e[j] * s);
+        o.store(to + at);
+    } else {
+        for (int j = at; j < c; ++j) to[j] = to_elem<E>((float)from[j] * s);
+    }
 }
 
+template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
+hipError_t launch_held(const RowArgs<E> &a, hipStream_t st) {
+    constexpr int ROWS = rows_threads(THREADS) / THREADS;
+    hipLaunchKernelGGL((rows_kernel<E, NORM, EIGHT, THREADS, CHUNKS>), dim3((unsigned)((a.N + ROWS - 1) / ROWS)),
+                       dim3(rows_threads(THREADS)), 0, st, a);
+    return hipGetLastError();
+}
+// Two chunks a thread while that gives threads enough: more loads in flight than with one,
+// more threads than with four.  us by threads x chunks of a row, norm with residual to 8
+// bits, bf16: 16384 x 4096 256 x 2 81.5, 128 x 4 83.4, 512 x 1 83.6, 64 x 8 92.3; 25728 x
+// 1024 64 x 2 36.4, 256 x 1 47.1; 32768 x 64 8 x 1 5.6, 64 x 1 14.7; 20000 x 512 32 x 2
+// 14.7, 64 x 1 16.0, 128 x 1 19.1; 8192 x 11008 512 x 4 114.8, 256 x 8 114.9, 1024 x 2 141.6;
+// few rows take 3.6 to 5 us with all of them.
 template <typename E, bool NORM, bool EIGHT> hipError_t launch_rows(const RowArgs<E> &a, hipStream_t st) {
     if (a.N <= 0) return hipSuccess;
-    hipLaunchKernelGGL((rows_kernel<E, NORM, EIGHT>), dim3((unsigned)a.N), dim3(kRowThreads), 0, st, a);
+    constexpr int V = Chunk<E>::V;
+    const int64_t chunks = a.c / V;
+    if (chunks <= 8) return launch_held<E, NORM, EIGHT, 8, 1>(a, st);
+    if (chunks <= 32) return launch_held<E, NORM, EIGHT, 16, 2>(a, st);
+    if (chunks <= 64) return launch_held<E, NORM, EIGHT, 32, 2>(a, st);
+    if (chunks <= 128) return launch_held<E, NORM, EIGHT, 64, 2>(a, st);
+    if (chunks <= 256) return launch_held<E, NORM, EIGHT, 128, 2>(a, st);
+    if (chunks <= 512) return launch_held<E, NORM, EIGHT, 256, 2>(a, st);
+    if (chunks <= 1024) return launch_held<E, NORM, EIGHT, 512, 2>(a, st);
+    if (chunks <= 2048) return launch_held<E, NORM, EIGHT, 512, 4>(a, st);
+    if (chunks <= 4096) return launch_held<E, NORM, EIGHT, 1024, 4>(a, st);
+    if (chunks <= 8192) return launch_held<E, NORM, EIGHT, 1024, 8>(a, st);
+    if constexpr (V == 4) return launch_held<E, NORM, EIGHT, 1024, 16>(a, st);
+    return hipErrorInvalidValue;  // longer rows are refused
+}
+
+template <typename E, int THREADS>
+hipError_t launch_back(const i8 *Q, int64_t ldq, const float *scales, int64_t N, int64_t c, E *X, int64_t ldx, hipStream_t st) {
+    constexpr int ROWS = 256 / THREADS, PIECE = Chunk<E>::V * THREADS;
+    hipLaunchKernelGGL((dequantize_kernel<E, THREADS>),
+                       dim3((unsigned)((N + ROWS - 1) / ROWS), (unsigned)((c + PIECE - 1) / PIECE)), dim3(256), 0, st, Q, ldq,
+                       scales, N, (int)c, X, ldx);
     return hipGetLastError();
 }
 
@@ -117,8 +302,13 @@ template <typename E>
 hipError_t launch_dequantize(const i8 *Q, int64_t ldq, const float *scales, int64_t N, int64_t c, E *X, int64_t ldx,
                              hipStream_t st) {
     if (N <= 0) return hipSuccess;
-    hipLaunchKernelGGL((dequantize_kernel<E>), dim3((unsigned)N), dim3(kRowThreads), 0, st, Q, ldq, scales, c, X, ldx);
-    return hipGetLastError();
+    // us by threads of a piece, bf16: 25728 x 200 16 4.9, 64 6.0, 256 9.5; 25728 x 1024 64
+    // 15.5, 256 18.6; 16384 x 4096 256 33.6, 64 41.2
+    constexpr int V = Chunk<E>::V;
+    if (c <= 16 * V) return launch_back<E, 16>(Q, ldq, scales, N, c, X, ldx, st);
+    if (c <= 32 * V) return launch_back<E, 32>(Q, ldq, scales, N, c, X, ldx, st);
+    if (c <= 128 * V) return launch_back<E, 64>(Q, ldq, scales, N, c, X, ldx, st);
+    return launch_back<E, 256>(Q, ldq, scales, N, c, X, ldx, st);
 }
 
 template hipError_t launch_norm<bf16>(const RowArgs<bf16> &, hipStream_t);

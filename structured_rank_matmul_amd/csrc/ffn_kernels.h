@@ -22,7 +22,9 @@ enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSil
 // integers, the scale of every token and of every weight row.
 template <typename E, typename O> struct Operands {
     typedef E Bias;
-    struct Scales {};
+    struct Scales {
+        static constexpr const float *x = nullptr, *w0 = nullptr, *w1 = nullptr;
+    };
 };
 template <typename O> struct Operands<i8, O> {
     typedef O Bias;

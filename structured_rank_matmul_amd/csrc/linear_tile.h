@@ -258,7 +258,9 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
     const Tile tile = pick_tile(sizeof(E), GATED, a.M, a.N, a.K * (int64_t)sizeof(E));
     if constexpr (sizeof(E) != 4) {
         if (tile == T256x256) return launch_big<E, O, GATED, 8>(a, st);
-        if (tile == T224x256) return launch_big<E, O, GATED, 7>(a, st);
+        if constexpr (sizeof(E) == 2) {
+            if (tile == T224x256) return launch_big<E, O, GATED, 7>(a, st);
+        }
         if (tile == T192x256) return launch_big<E, O, GATED, 6>(a, st);
         switch (tile) {
         case T32x64: return launch_tile<E, O, 32, GATED ? 32 : 64, 1, GATED ? 1 : 2, GATED ? 4 : 2, 5, 2, GATED>(a, st);

@@ -401,10 +401,16 @@ dyra_status dyra_dequantize(const int8_t *Q, int64_t ldq, const float *scales, i
  * [c2], or NULL; residual and Y device, out_dtype, [N][c2].  The sums are exact, in 32-bit
  * integers.  c1, ldx and ldw are multiples of 16 (DYRA_ERR_SHAPE, DYRA_ERR_ALIGN), ldx, ldw
  * <= 2^20; everything else as for dyra_linear.
+ *
+ * workspace device, 16-byte aligned, or NULL.  With dyra_quantized_workspace_bytes() bytes a
+ * product of long rows and few tiles is shared by more workgroups (faster, the same bits);
+ * with fewer, or NULL, it is not.  Contents on entry ignored; calls that overlap in time need
+ * separate ones.
  */
 dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wt, int64_t ldw,
                                   const float *w_scales, int64_t N, int64_t c1, int64_t c2, const void *bias, dyra_act act,
-                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *stream);
+                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /*
  * dyra_gated on 8-bit integers: both products of H = act(X Wg + bias_g) * (X Wu + bias_u) as
@@ -414,7 +420,11 @@ dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_s
 dyra_status dyra_gated_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wg, const float *g_scales,
                                  const int8_t *Wu, const float *u_scales, int64_t ldw, int64_t N, int64_t c1, int64_t c2,
                                  const void *bias_g, const void *bias_u, dyra_act act, dyra_dtype out_dtype, void *H,
-                                 int64_t ldh, void *stream);
+                                 int64_t ldh, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace that dyra_linear_quantized (gated 0) or dyra_gated_quantized makes use of; 0 where it is of none, and for
+   sizes that they refuse.  At most 64 MiB. */
+size_t dyra_quantized_workspace_bytes(int64_t N, int64_t c1, int64_t c2, int32_t gated);
 
 typedef enum {
     DYRA_SCORE_SOFTMAX = 0,  /* exp(l_e) / sum over all experts */

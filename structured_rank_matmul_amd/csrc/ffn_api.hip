@@ -122,6 +122,21 @@ template <typename E, typename O, bool GATED> dyra_status run(const dyra::Linear
     return hip_status(dyra::launch_linear<E, O, GATED>(a, st));
 }
 
+// How K of such a product is split where there is a workspace.
+dyra::Split split_of(bool gated, int64_t N, int64_t c1, int64_t c2) {
+    if (N <= dyra::kSkinnyTokens || dyra::takes_narrow(1, gated, N, c2)) return {dyra::T32x64, 1, 0};
+    return dyra::pick_split(gated, N, c2, c1);
+}
+template <typename O, bool GATED>
+dyra_status run_quantized(const dyra::LinearArgs<i8, O> &a, void *work, size_t bytes, hipStream_t st) {
+    if (work) {
+        const dyra::Split s = split_of(GATED, a.M, a.K, a.N);
+        if (s.parts > 1 && bytes >= (size_t)dyra::split_bytes(GATED, a.M, a.N, s.parts))
+            return hip_status(dyra::launch_split<O, GATED>(a, s, (int32_t *)work, st));
+    }
+    return run<i8, O, GATED>(a, st);
+}
+
 template <typename E, typename O, bool GATED>
 dyra_status run_linear(const void *X, int64_t ldx, const void *W0, const void *W1, int64_t ldw, int64_t N, int64_t c1,
                        int64_t c2, const void *b0, const void *b1, dyra_act act, const void *R, int64_t ldr, void *Y,
@@ -225,9 +240,15 @@ dyra_status dyra_dequantize(const int8_t *Q, int64_t ldq, const float *scales, i
                                          : dyra::launch_dequantize<float>(Q, ldq, scales, N, c, (float *)X, ldx, st));
 }
 
+size_t dyra_quantized_workspace_bytes(int64_t N, int64_t c1, int64_t c2, int32_t gated) {
+    if (N <= 0 || c1 <= 0 || c2 <= 0 || N > kMaxDim || c2 > kMaxDim || c1 > kMaxRow8 || c1 % 16 != 0) return 0;
+    return (size_t)dyra::split_bytes(gated != 0, N, c2, split_of(gated != 0, N, c1, c2).parts);
+}
+
 dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wt, int64_t ldw,
                                   const float *w_scales, int64_t N, int64_t c1, int64_t c2, const void *bias, dyra_act act,
-                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *stream) {
+                                  const void *residual, int64_t ldr, dyra_dtype out_dtype, void *Y, int64_t ldy, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
     bool empty;
     const dyra_status s = check_quantized(X, ldx, x_scales, Wt, Wt, ldw, w_scales, w_scales, N, c1, c2, bias, nullptr, act, Y, ldy, out_dtype, &empty);
     if (s != DYRA_OK) return s;
@@ -235,11 +256,13 @@ dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_s
     if (empty) return DYRA_OK;
     if (!aligned(residual, size_of(out_dtype))) return DYRA_ERR_ALIGN;
     if (among(Y, {X, x_scales, Wt, w_scales, bias}) || other_rows(Y, ldy, N, residual, ldr)) return DYRA_ERR_ARG;
+    if (!aligned(workspace, 16)) return DYRA_ERR_ALIGN;
+    if (among(workspace, {Y, X, x_scales, Wt, w_scales, bias, residual})) return DYRA_ERR_ARG;
     if (!residual) ldr = 0;
     auto go = [&](auto o) {
         typedef decltype(o) O;
-        return run<i8, O, false>({X, ldx, Wt, nullptr, ldw, N, c2, c1, (const O *)bias, nullptr, (const O *)residual, ldr, (O *)Y, ldy, (int)act,
-                                  {x_scales, w_scales, nullptr}}, (hipStream_t)stream);
+        return run_quantized<O, false>({X, ldx, Wt, nullptr, ldw, N, c2, c1, (const O *)bias, nullptr, (const O *)residual, ldr, (O *)Y, ldy, (int)act,
+                                        {x_scales, w_scales, nullptr}}, workspace, workspace_bytes, (hipStream_t)stream);
     };
     return out_dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
 }
@@ -247,15 +270,17 @@ dyra_status dyra_linear_quantized(const int8_t *X, int64_t ldx, const float *x_s
 dyra_status dyra_gated_quantized(const int8_t *X, int64_t ldx, const float *x_scales, const int8_t *Wg, const float *g_scales,
                                  const int8_t *Wu, const float *u_scales, int64_t ldw, int64_t N, int64_t c1, int64_t c2,
                                  const void *bias_g, const void *bias_u, dyra_act act, dyra_dtype out_dtype, void *H,
-                                 int64_t ldh, void *stream) {
+                                 int64_t ldh, void *workspace, size_t workspace_bytes, void *stream) {
     bool empty;
     const dyra_status s = check_quantized(X, ldx, x_scales, Wg, Wu, ldw, g_scales, u_scales, N, c1, c2, bias_g, bias_u, act, H, ldh, out_dtype, &empty);
     if (s != DYRA_OK || empty) return s;
     if (among(H, {X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u})) return DYRA_ERR_ARG;
+    if (!aligned(workspace, 16)) return DYRA_ERR_ALIGN;
+    if (among(workspace, {H, X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u})) return DYRA_ERR_ARG;
     auto go = [&](auto o) {
         typedef decltype(o) O;
-        return run<i8, O, true>({X, ldx, Wg, Wu, ldw, N, c2, c1, (const O *)bias_g, (const O *)bias_u, nullptr, 0, (O *)H, ldh, (int)act,
-                                 {x_scales, g_scales, u_scales}}, (hipStream_t)stream);
+        return run_quantized<O, true>({X, ldx, Wg, Wu, ldw, N, c2, c1, (const O *)bias_g, (const O *)bias_u, nullptr, 0, (O *)H, ldh, (int)act,
+                                       {x_scales, g_scales, u_scales}}, workspace, workspace_bytes, (hipStream_t)stream);
     };
     return out_dtype == DYRA_BF16 ? go(bf16{}) : go(float{});
 }

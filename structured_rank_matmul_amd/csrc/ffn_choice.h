@@ -70,12 +70,58 @@ inline Tile pick_tile(int elem, bool gated, int64_t M, int64_t N, int64_t row_by
     Tile best = T32x64;
     double cost = 1e300;
     for (int i = T32x64; i <= (elem != 4 ? T256x256 : T128x128); ++i) {
+        if (elem == 1 && i == T224x256) continue;  // not made: its epilogue does not fit the registers
         const TileCost &t = kTiles[i];
         const double rounds = std::ceil(std::ceil((double)M / t.bm) * std::ceil(rows / t.bn) / 256.0);
         const double c = rounds * (slabs * (elem != 4 ? t.slab : t.slab_f32) + t.once);
         if (c < cost) {
             cost = c;
             best = (Tile)i;
+        }
+    }
+    return best;
+}
+
+// 8-bit operands, whose sums are exact: K in `parts` that a product's tiles are made of by
+// as many workgroups each, joined by a second kernel.  It pays for long rows and few tiles;
+// the second kernel and the workspace cost 6 us.  The times of the tiles above are
+// those of short rows: over long ones the smaller tiles took up to 1.5 times as long, parts of
+// them 1.2 times (fitted to 90 products of 33 to 8000 tokens: the choice is 0.7 % behind
+// the best of all on average, never to split 7 %).  us, whole | split: 186 x 12416 -> 188
+// 19.2 | 10.3, 64 x 14336 -> 4096 28.7 | 19.2, 185 x 11072 -> 1600 19.2 | 14.4, gated 1102 x
+// 10288 -> 456 38.9 | 28.0, 166 x 10320 -> 3968 54.9 | 43.9; left whole: 64 x 4096 -> 4096 8.9
+// | 10.8, 512 x 4096 -> 4096 14.9 | 22.8, 583 x 5808 -> 3957 31.7 | 32.2.
+struct Split {
+    Tile tile;
+    int parts;   // 1: no split
+    int slabs;   // of a part (the last may have fewer)
+};
+// Sums of a row in the workspace, and what one call may take of it.
+constexpr int64_t split_row(int64_t N) { return (N + 7) / 8 * 8; }
+constexpr int64_t kSplitBytesMost = int64_t{64} << 20;
+inline int64_t split_bytes(bool gated, int64_t M, int64_t N, int parts) {
+    return parts > 1 ? (int64_t)parts * (gated ? 2 : 1) * M * split_row(N) * 4 : 0;
+}
+inline Split pick_split(bool gated, int64_t M, int64_t N, int64_t row_bytes) {
+    const double rows = (double)N * (gated ? 2 : 1), slabs = std::ceil((double)row_bytes / 128.0);
+    const Tile whole = pick_tile(1, gated, M, N, row_bytes);
+    const double count = std::ceil((double)M / kTiles[whole].bm) * std::ceil(rows / kTiles[whole].bn);
+    Split best{whole, 1, (int)slabs};
+    double cost = 0.9 * std::ceil(count / 256.0) * (slabs * kTiles[whole].slab * (whole <= T128x128 ? 1.5 : 1.0) + kTiles[whole].once);
+    for (int i = T64x64; i <= T128x256; ++i) {
+        const TileCost &t = kTiles[i];
+        const double tiles = std::ceil((double)M / t.bm) * std::ceil(rows / t.bn);
+        for (int want = 2; want <= 16; ++want) {
+            // whole stages of up to two slabs; at least 8 slabs a part
+            const int per = 2 * (int)std::ceil(slabs / want / 2.0), parts = (int)std::ceil(slabs / per);
+            if (per < 8 || parts < 2) break;
+            const int64_t bytes = split_bytes(gated, M, N, parts);
+            if (bytes > kSplitBytesMost) break;
+            const double c = std::ceil(tiles * parts / 256.0) * (per * t.slab * 1.2 + t.once) + 6000.0 + (double)bytes / 4000.0;
+            if (c < cost) {
+                cost = c;
+                best = {(Tile)i, parts, per};
+            }
         }
     }
     return best;

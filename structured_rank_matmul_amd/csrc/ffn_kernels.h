@@ -53,6 +53,9 @@ template <typename E, typename O> struct LinearArgs {
 };
 
 template <typename E, typename O, bool GATED> hipError_t launch_linear(const LinearArgs<E, O> &a, hipStream_t st);
+// 8-bit operands with K in parts (s.parts > 1): split_bytes() of `work`.
+template <typename O, bool GATED>
+hipError_t launch_split(const LinearArgs<i8, O> &a, const Split &s, int32_t *work, hipStream_t st);
 // Few tokens: the weights are streamed once.
 template <typename E, typename O, bool GATED> hipError_t launch_skinny(const LinearArgs<E, O> &a, hipStream_t st);
 // Few features (up to 32, gated 16) of many tokens: X is streamed.

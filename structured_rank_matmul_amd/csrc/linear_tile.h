@@ -57,9 +57,17 @@ template <typename E, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bo
     static_assert(TF % 2 == 0 && TM >= 1 && BF % 32 == 0 && NS * STAGE <= 160 * 1024, "tile shape");
 };
 
-template <typename E, typename O, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED>
+// The workgroups of a tile take `slabs` slabs of K each, `count` of them, and their integer
+// sums go to `sums` ([part][gate, up][token][split_row(N)]) instead of through the epilogue.
+template <bool PARTS> struct Parts {};
+template <> struct Parts<true> {
+    int count, slabs;
+    int32_t *sums;
+};
+
+template <typename E, typename O, int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED, bool PARTS = false>
 __global__ __launch_bounds__(64 * WM * WN * KS, (TileShape<E, BM, BF, WM, WN, KS, NS, SL, GATED>::PER_CU * WM * WN * KS / 4)) void
-linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
+linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd, Parts<PARTS> parts) {
     using S = TileShape<E, BM, BF, WM, WN, KS, NS, SL, GATED>;
     typedef typename Sums<E>::type Acc;
     __shared__ __align__(16) char smem[NS * S::STAGE];
@@ -70,7 +78,18 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
     // workgroup ids are dealt round-robin over the 8 XCDs; each XCD walks a
     // contiguous band of tiles, down the tokens first, so tiles that share
     // weights share an L2
-    const int tile = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+    int tile = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+    int part = 0;
+    if constexpr (PARTS) {  // all tiles of a part, then of the next
+        if (tile >= ntiles * parts.count) return;
+        part = tile / ntiles;
+        tile -= part * ntiles;
+        const int64_t k0 = (int64_t)part * parts.slabs * (128 / (int64_t)sizeof(E));
+        a.X += k0;
+        a.W0 += k0;
+        a.W1 += GATED ? k0 : 0;
+        a.K = std::min<int64_t>(a.K - k0, parts.slabs * (128 / (int64_t)sizeof(E)));
+    }
     if (tile >= ntiles) return;
     const int tiles_m = ntiles / tiles_n;
     const int64_t row0 = (int64_t)(tile % tiles_m) * BM;
@@ -195,6 +214,27 @@ linear_tile_kernel(LinearArgs<E, O> a, int tiles_n, int ntiles, int per_xcd) {
                 for (int j = 0; j < S::TN; ++j)
                     sum[i][j] += *reinterpret_cast<const Acc *>(place(kg + S::OWNERS * i, o) + j * 1024);
     }
+    if constexpr (PARTS) {
+        const int64_t row = split_row(a.N);
+#pragma unroll
+        for (int p = 0; p < S::TF / 2; ++p) {
+            const int64_t c = col0 + wn * S::TF * 16 + 32 * p + 8 * g;
+            if (c >= a.N) continue;
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const int64_t t = row0 + (wm * S::TM + S::OWNERS * i + kg) * 16 + i16;
+                if (t >= a.M) continue;
+#pragma unroll
+                for (int plane = 0; plane < (GATED ? 2 : 1); ++plane) {
+                    int32_t *const to = parts.sums + ((part * (GATED ? 2 : 1) + plane) * a.M + t) * row + c;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<Acc *>(to + 4 * j) = sum[i][S::TF * plane + 2 * p + j];
+                }
+            }
+        }
+        return;
+    }
     // ---- epilogue: 8 consecutive features of one token per pair of blocks
 #pragma unroll
     for (int p = 0; p < S::TF / 2; ++p) {
@@ -247,7 +287,53 @@ hipError_t launch_tile(const LinearArgs<E, O> &a, hipStream_t st) {
     if (ntiles > (int64_t)INT32_MAX - 8) return hipErrorInvalidValue;
     const int64_t per_xcd = (ntiles + 7) / 8;
     hipLaunchKernelGGL((linear_tile_kernel<E, O, BM, BF, WM, WN, KS, NS, SL, GATED>), dim3((unsigned)(8 * per_xcd)),
-                       dim3(64 * WM * WN * KS), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd);
+                       dim3(64 * WM * WN * KS), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd, Parts<false>{});
+    return hipGetLastError();
+}
+
+// The parts' sums joined, and the epilogue: 8 features of a token a thread.
+template <typename O, bool GATED>
+__global__ __launch_bounds__(256) void join_parts_kernel(LinearArgs<i8, O> a, int parts, const int32_t *sums) {
+    const int64_t row = split_row(a.N), at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = at / (row / 8), c = (at - t * (row / 8)) * 8;
+    if (t >= a.M) return;
+    constexpr int PLANES = GATED ? 2 : 1;
+    i32x4 sum[PLANES][2] = {};
+#pragma unroll 4
+    for (int part = 0; part < parts; ++part)
+#pragma unroll
+        for (int plane = 0; plane < PLANES; ++plane)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                sum[plane][j] += *reinterpret_cast<const i32x4 *>(sums + (((int64_t)part * PLANES + plane) * a.M + t) * row + c + 4 * j);
+    const int have = (int)std::min<int64_t>(8, a.N - c);
+    float b0[8] = {}, b1[8] = {}, s0[8], s1[8] = {}, v[8];
+    if (a.b0) load_row(a.b0 + c, b0, have);
+    if (GATED && a.b1) load_row(a.b1 + c, b1, have);
+    const float sx = a.scale.x[t];
+    load_row(a.scale.w0 + c, s0, have);
+    if constexpr (GATED) load_row(a.scale.w1 + c, s1, have);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = biased(sum[0][q >> 2][q & 3], sx, s0[q], b0[q]);
+    activate<sizeof(O) == 4>(v, a.act);
+    if constexpr (GATED) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= biased(sum[PLANES - 1][q >> 2][q & 3], sx, s1[q], b1[q]);
+    } else if (a.R) {
+        add_row(v, a.R + t * a.ldr + c, have);
+    }
+    store_row(a.Y + t * a.ldy + c, v, have);
+}
+
+// (the operands' part of the arguments: the sums do not depend on O)
+template <int BM, int BF, int WM, int WN, int KS, int NS, int SL, bool GATED>
+hipError_t launch_parts(const LinearArgs<i8, float> &a, const Split &s, int32_t *work, hipStream_t st) {
+    const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BF - 1) / BF;
+    const int64_t ntiles = tiles_m * tiles_n, units = ntiles * s.parts;
+    if (units > (int64_t)INT32_MAX - 8) return hipErrorInvalidValue;
+    const int64_t per_xcd = (units + 7) / 8;
+    hipLaunchKernelGGL((linear_tile_kernel<i8, float, BM, BF, WM, WN, KS, NS, SL, GATED, true>), dim3((unsigned)(8 * per_xcd)),
+                       dim3(64 * WM * WN * KS), 0, st, a, (int)tiles_n, (int)ntiles, (int)per_xcd, Parts<true>{s.parts, s.slabs, work});
     return hipGetLastError();
 }
 
@@ -280,6 +366,24 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
         default: return launch_tile<E, O, 128, GATED ? 64 : 128, GATED ? 4 : 2, GATED ? 2 : 4, 1, 2, 1, GATED>(a, st);
         }
     }
+}
+
+// K in parts.  us without | with (the tiles of ffn_choice.h, join included): see there.
+template <typename O, bool GATED>
+hipError_t launch_split(const LinearArgs<i8, O> &a, const Split &s, int32_t *work, hipStream_t st) {
+    if (a.M <= 0 || a.N <= 0) return hipSuccess;
+    const LinearArgs<i8, float> sums{a.X, a.ldx, a.W0, a.W1, a.ldw, a.M, a.N, a.K, nullptr, nullptr, nullptr, 0, nullptr, 0, 0, {}};
+    hipError_t e;
+    switch (s.tile) {
+    case T64x64: e = launch_parts<64, GATED ? 32 : 64, 1, GATED ? 1 : 2, 4, 4, 2, GATED>(sums, s, work, st); break;
+    case T64x128: e = launch_parts<64, GATED ? 64 : 128, 1, 2, 4, 3, 2, GATED>(sums, s, work, st); break;
+    case T128x128: e = launch_parts<128, GATED ? 64 : 128, 2, 2, 2, 4, 1, GATED>(sums, s, work, st); break;
+    default: e = launch_parts<128, GATED ? 128 : 256, 2, 2, 2, 3, 1, GATED>(sums, s, work, st);
+    }
+    if (e != hipSuccess) return e;
+    const int64_t threads = a.M * (split_row(a.N) / 8);  // split_bytes() keeps it below 2^21
+    hipLaunchKernelGGL((join_parts_kernel<O, GATED>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, a, s.parts, work);
+    return hipGetLastError();
 }
 
 }  // namespace dyra

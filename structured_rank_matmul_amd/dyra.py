@@ -30,6 +30,7 @@ EXPORTED = (
     "dyra_forward_noalloc", "dyra_noalloc_scratch_bytes",
     "dyra_linear", "dyra_gated", "dyra_route", "dyra_moe", "dyra_moe_workspace_bytes",
     "dyra_norm", "dyra_norm_quantize", "dyra_quantize", "dyra_dequantize", "dyra_linear_quantized", "dyra_gated_quantized",
+    "dyra_quantized_workspace_bytes",
 )
 
 
@@ -109,10 +110,14 @@ def load() -> ctypes.CDLL:
     L.dyra_quantize.restype = ctypes.c_int
     L.dyra_dequantize.argtypes = [vp, i64, vp, i64, i64, en, vp, i64, vp]
     L.dyra_dequantize.restype = ctypes.c_int
-    L.dyra_linear_quantized.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, en, vp, i64, en, vp, i64, vp]
+    L.dyra_linear_quantized.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, en, vp, i64, en, vp, i64, vp,
+                                        ctypes.c_size_t, vp]
     L.dyra_linear_quantized.restype = ctypes.c_int
-    L.dyra_gated_quantized.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, en, en, vp, i64, vp]
+    L.dyra_gated_quantized.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, en, en, vp, i64, vp,
+                                       ctypes.c_size_t, vp]
     L.dyra_gated_quantized.restype = ctypes.c_int
+    L.dyra_quantized_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.dyra_quantized_workspace_bytes.restype = ctypes.c_size_t
     L.dyra_stage_name.argtypes = [vp, i64, i32]
     L.dyra_stage_name.restype = ctypes.c_char_p
     _lib = L
@@ -683,14 +688,41 @@ def dyra_dequantize(Q, scales, out_dtype=None, X=None, stream=None):
     return X
 
 
+def dyra_quantized_workspace_bytes(N: int, c1: int, c2: int, gated: bool = False) -> int:
+    return int(load().dyra_quantized_workspace_bytes(int(N), int(c1), int(c2), 1 if gated else 0))
+
+
+_split_bytes = {}   # what the function above answers, by its arguments
+
+
+def _split_workspace(workspace, X, dev, N, c1, c2, gated, stream):
+    """(tensor or None, address or None, bytes) of a product's workspace."""
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on GPU {dev}")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    key = (N, c1, c2, gated)
+    size = _split_bytes.get(key)
+    if size is None:
+        if len(_split_bytes) > 10000:
+            _split_bytes.clear()
+        size = _split_bytes[key] = dyra_quantized_workspace_bytes(N, c1, c2, gated)
+    if size == 0:
+        return None, None, 0
+    workspace = _new((size,), _types()[0], X, stream)
+    return workspace, workspace.data_ptr(), size
+
+
 def dyra_linear_quantized(X, x_scales, Wt, w_scales, bias=None, act: str = "none", residual=None, out_dtype=None, Y=None,
-                          stream=None):
+                          workspace=None, stream=None):
     """dyra_linear on 8-bit integers: X int8 [N, c1] with a scale for each token, Wt int8 [c2, c1] with a scale for each
-    feature (both float32); bias, residual and Y in out_dtype (bfloat16 by default)."""
+    feature (both float32); bias, residual and Y in out_dtype (bfloat16 by default).  Without a workspace one of
+    dyra_quantized_workspace_bytes is allocated (0 for most sizes); the results do not depend on it."""
     N, c1, ldx, dev = _input(X)
     st = _stream_on(dev, stream)
     if st is None:
-        return _with_device(dev, dyra_linear_quantized, X, x_scales, Wt, w_scales, bias, act, residual, out_dtype, Y, stream)
+        return _with_device(dev, dyra_linear_quantized, X, x_scales, Wt, w_scales, bias, act, residual, out_dtype, Y, workspace,
+                            stream)
     i8, f32, bf16 = _types()
     if X.dtype != i8:
         raise ValueError(f"X must be int8, got {X.dtype}")
@@ -708,22 +740,23 @@ def dyra_linear_quantized(X, x_scales, Wt, w_scales, bias=None, act: str = "none
         Y, ldy = _new((N, c2), out, X, stream), c2
     else:
         ldy = _matrix(Y, "Y", dev, N, c2, out)
+    workspace, wp, size = _split_workspace(workspace, X, dev, N, c1, c2, False, stream)
     status = (_lib or load()).dyra_linear_quantized(X.data_ptr(), ldx, sx, Wt.data_ptr(), ldw, sw, N, c1, c2, b, acode, r, ldr,
-                                                    code, Y.data_ptr(), ldy, st)
+                                                    code, Y.data_ptr(), ldy, wp, size, st)
     if status != 0:
         raise DyraError(status, "dyra_linear_quantized")
     return Y
 
 
 def dyra_gated_quantized(X, x_scales, Wg, g_scales, Wu, u_scales, bias_g=None, bias_u=None, act: str = "silu",
-                         out_dtype=None, H=None, stream=None):
+                         out_dtype=None, H=None, workspace=None, stream=None):
     """dyra_gated on 8-bit integers: Wg and Wu int8 [c2, c1] with one row stride and their scales for each feature; biases
-    and H in out_dtype (bfloat16 by default)."""
+    and H in out_dtype (bfloat16 by default); workspace as for dyra_linear_quantized."""
     N, c1, ldx, dev = _input(X)
     st = _stream_on(dev, stream)
     if st is None:
         return _with_device(dev, dyra_gated_quantized, X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u, act, out_dtype,
-                            H, stream)
+                            H, workspace, stream)
     i8, f32, bf16 = _types()
     if X.dtype != i8:
         raise ValueError(f"X must be int8, got {X.dtype}")
@@ -742,8 +775,9 @@ def dyra_gated_quantized(X, x_scales, Wg, g_scales, Wu, u_scales, bias_g=None, b
         H, ldh = _new((N, c2), out, X, stream), c2
     else:
         ldh = _matrix(H, "H", dev, N, c2, out)
+    workspace, wp, size = _split_workspace(workspace, X, dev, N, c1, c2, True, stream)
     status = (_lib or load()).dyra_gated_quantized(X.data_ptr(), ldx, sx, Wg.data_ptr(), sg, Wu.data_ptr(), su, ldw, N, c1, c2,
-                                                   bg, bu, acode, code, H.data_ptr(), ldh, st)
+                                                   bg, bu, acode, code, H.data_ptr(), ldh, wp, size, st)
     if status != 0:
         raise DyraError(status, "dyra_gated_quantized")
     return H

@@ -571,7 +571,8 @@ def test_binding_refuses_mismatched_tensors():
            lambda: lin(q, s, w, sw, residual=torch.zeros(4, 8, device="cuda")), lambda: lin(q, s, w, sw, out_dtype=torch.float16),
            lambda: lin(q, s, w, sw, out_dtype=torch.int8), lambda: lin(q.view(torch.uint8), s, w, sw), lambda: lin(q, s, w.view(torch.uint8), sw),
            lambda: lin(q, s, w, sw, Y=torch.zeros(4, 8, device="cuda")), lambda: lin(q.cpu(), s, w, sw), lambda: lin(q.t(), s, w, sw),
-           lambda: lin(q, torch.ones(8, device="cuda")[::2], w, sw),
+           lambda: lin(q, torch.ones(8, device="cuda")[::2], w, sw), lambda: lin(q, s, w, sw, workspace=torch.zeros(64)),
+           lambda: gat(q, s, w, sw, w, sw, workspace=torch.zeros(64, device="cuda")[::2]),
            lambda: gat(q, s, w, sw, w[:4], sw), lambda: gat(q, s, w, sw, torch.zeros(8, 128, dtype=torch.int8, device="cuda")[:, :64], sw),
            lambda: gat(q, s, w, sw, w, s), lambda: gat(q, s, w, s, w, sw), lambda: gat(x, s, w, sw, w, sw),
            lambda: dyra.dyra_norm(q), lambda: dyra.dyra_norm(x.half()), lambda: dyra.dyra_norm(x, torch.ones(63, device="cuda")),

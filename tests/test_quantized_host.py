@@ -28,13 +28,13 @@ def dequantize(Q=P, ldq=64, scales=2 * P, N=8, c=61, dtype=BF16, X=3 * P, ldx=64
 
 
 def linear(X=P, ldx=64, sx=2 * P, Wt=3 * P, ldw=64, sw=4 * P, N=8, c1=64, c2=48, bias=None, act=0, res=None, ldr=0, out=BF16,
-           Y=5 * P, ldy=48):
-    return dyra.load().dyra_linear_quantized(X, ldx, sx, Wt, ldw, sw, N, c1, c2, bias, act, res, ldr, out, Y, ldy, None)
+           Y=5 * P, ldy=48, ws=None, size=0):
+    return dyra.load().dyra_linear_quantized(X, ldx, sx, Wt, ldw, sw, N, c1, c2, bias, act, res, ldr, out, Y, ldy, ws, size, None)
 
 
 def gated(X=P, ldx=64, sx=2 * P, Wg=3 * P, sg=4 * P, Wu=5 * P, su=6 * P, ldw=64, N=8, c1=64, c2=48, bg=None, bu=None, act=4,
-          out=BF16, H=7 * P, ldh=48):
-    return dyra.load().dyra_gated_quantized(X, ldx, sx, Wg, sg, Wu, su, ldw, N, c1, c2, bg, bu, act, out, H, ldh, None)
+          out=BF16, H=7 * P, ldh=48, ws=None, size=0):
+    return dyra.load().dyra_gated_quantized(X, ldx, sx, Wg, sg, Wu, su, ldw, N, c1, c2, bg, bu, act, out, H, ldh, ws, size, None)
 
 
 def test_empty_calls_are_no_ops():
@@ -92,14 +92,14 @@ PRODUCTS = [(DTYPE, dict(out=2)), (ARG, dict(act=5)), (ARG, dict(act=-1)), (SHAP
             (SHAPE, dict(N=(1 << 25) + 1)), (SHAPE, dict(c2=(1 << 25) + 1)), (SHAPE, dict(c1=56)), (SHAPE, dict(c1=65552, ldx=65552, ldw=65552)),
             (SHAPE, dict(ldx=(1 << 20) + 16)), (SHAPE, dict(ldw=(1 << 20) + 16)), (ARG, dict(ldx=48)), (ARG, dict(ldw=48)),
             (ALIGN, dict(ldx=72)), (ALIGN, dict(ldw=72)), (ARG, dict(X=None)), (ARG, dict(sx=None)), (ALIGN, dict(X=P + 8)),
-            (ALIGN, dict(sx=P + 2))]
+            (ALIGN, dict(sx=P + 2)), (ALIGN, dict(ws=P + 8, size=1 << 20))]
 
 
 @pytest.mark.parametrize("status,kw", PRODUCTS + [
     (ARG, dict(ldy=47)), (ARG, dict(Wt=None)), (ARG, dict(sw=None)), (ARG, dict(Y=None)), (ALIGN, dict(Wt=P + 8)), (ALIGN, dict(sw=P + 1)),
     (ALIGN, dict(Y=P + 1)), (ALIGN, dict(out=F32, Y=P + 2)), (ALIGN, dict(bias=P + 1)), (ALIGN, dict(out=F32, bias=P + 2)),
     (ARG, dict(res=6 * P, ldr=47)), (ALIGN, dict(res=P + 1, ldr=48)), (ARG, dict(res=5 * P, ldr=56)), (ARG, dict(bias=5 * P))]
-    + [(ARG, dict(Y=i * P)) for i in (1, 2, 3, 4)])
+    + [(ARG, dict(Y=i * P)) for i in (1, 2, 3, 4)] + [(ARG, dict(ws=i * P, bias=6 * P, res=7 * P, ldr=48)) for i in range(1, 8)])
 def test_linear_refuses(status, kw):
     assert linear(**kw) == status
 
@@ -107,6 +107,14 @@ def test_linear_refuses(status, kw):
 @pytest.mark.parametrize("status,kw", PRODUCTS + [
     (ARG, dict(ldh=47)), (ARG, dict(H=None)), (ALIGN, dict(H=P + 1)), (ALIGN, dict(bg=P + 1)), (ALIGN, dict(bu=P + 1))]
     + [(ARG, {n: None}) for n in ("Wg", "sg", "Wu", "su")] + [(ALIGN, {n: P + 2}) for n in ("Wg", "sg", "Wu", "su")]
-    + [(ARG, dict(H=i * P)) for i in (1, 2, 3, 4, 5, 6)] + [(ARG, dict(bg=7 * P)), (ARG, dict(bu=7 * P))])
+    + [(ARG, dict(H=i * P)) for i in (1, 2, 3, 4, 5, 6)] + [(ARG, dict(bg=7 * P)), (ARG, dict(bu=7 * P))]
+    + [(ARG, dict(ws=i * P, bg=8 * P, bu=9 * P)) for i in range(1, 10)])
 def test_gated_refuses(status, kw):
     assert gated(**kw) == status
+
+
+@pytest.mark.parametrize("N,c1,c2", [(0, 14336, 64), (-1, 14336, 64), (64, 14328, 64), (64, 65552, 64), (64, 0, 64), (64, 14336, 0),
+                                     ((1 << 25) + 1, 14336, 64), (64, 14336, (1 << 25) + 1), (16, 14336, 4096), (4096, 14336, 4096)])
+def test_no_workspace_for_refused_sizes_and_where_none_is_used(N, c1, c2):
+    for gated_ in (0, 1):
+        assert dyra.load().dyra_quantized_workspace_bytes(N, c1, c2, gated_) == 0

@@ -54,8 +54,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t panel(const void *p, int64_t b
     const int n = bytes < (int64_t)kOutside - 1 ? (int)bytes : (int)(kOutside - 1);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00027000);
 }
+// ONCE: read by few workgroups, at the same time, and not soon again (non-temporal).  8-bit
+// weights of few tokens, us without | with: gated 16 x 4096 -> 14336 27.0 | 23.6, 64 x 4096 ->
+// 14336 28.5 | 25.6, 16 x 8192 -> 16384 27.9 | 24.7, 256 x 4096 -> 4096 12.7 | 12.4; where many
+// tiles share them (8000 x 4096 -> 64) 12.6 | 14.2.
+template <bool ONCE = false>
 __device__ __forceinline__ void buffer_to_lds16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char *lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, (int)voff, (int)soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, (int)voff, (int)soff, 0,
+                                             ONCE ? 2 : 0);
 }
 template <int N> __device__ __forceinline__ void wait_lds_and_vm() {
     // lgkmcnt(0) and vmcnt(N): gfx9 encoding, expcnt left at its maximum
@@ -180,12 +186,20 @@ template <typename T> __device__ __forceinline__ void add_row(float (&v)[8], con
     }
 }
 // Eight results of a row, of which the first `have` (0 .. 8) exist: a 16-byte store (two
-// for float32), or, in the last columns, one each of four, two and one element.
-__device__ __forceinline__ void store_row(float *p, const float (&v)[8], int have) {
+// for float32), or, in the last columns, one each of four, two and one element.  PASS: past
+// the L2 (non-temporal), for whole lines.
+template <bool PASS = false> __device__ __forceinline__ void store_row(float *p, const float (&v)[8], int have) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef f32x4 f32x4_any __attribute__((aligned(4)));
     typedef f32x2 f32x2_any __attribute__((aligned(4)));
     const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    if constexpr (PASS) {
+        if (have >= 8) {
+            __builtin_nontemporal_store(lo, reinterpret_cast<f32x4_any *>(p));
+            __builtin_nontemporal_store(hi, reinterpret_cast<f32x4_any *>(p + 4));
+            return;
+        }
+    }
     const bool four = have & 4, two = have & 2;
     if (have >= 8 || four) *reinterpret_cast<f32x4_any *>(p) = lo;
     if (have >= 8) {
@@ -196,13 +210,19 @@ __device__ __forceinline__ void store_row(float *p, const float (&v)[8], int hav
     if (two) *reinterpret_cast<f32x2_any *>(p + (have & 4)) = f32x2{rest[0], rest[1]};
     if (have & 1) p[have & 6] = two ? rest[2] : rest[0];
 }
-__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[8], int have) {
+template <bool PASS = false> __device__ __forceinline__ void store_row(bf16 *p, const float (&v)[8], int have) {
     typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
     typedef u32x2 u32x2_any __attribute__((aligned(2)));
     typedef unsigned u32_any __attribute__((aligned(2)));
     union { u32x4 u; bf16 e[8]; } w;
 #pragma unroll
     for (int q = 0; q < 8; ++q) w.e[q] = to_elem<bf16>(v[q]);
+    if constexpr (PASS) {
+        if (have >= 8) {
+            __builtin_nontemporal_store(w.u, reinterpret_cast<u32x4_any *>(p));
+            return;
+        }
+    }
     if (have >= 8) {
         *reinterpret_cast<u32x4_any *>(p) = w.u;
         return;

@@ -351,7 +351,10 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
                         }
                         if constexpr (RESIDUAL && ACT >= 0) r[i - i0][hw].add_to(v);
                         else if constexpr (RESIDUAL) add_row(v, a.R + t * a.ldr + c + 32 * hw, have);
-                        store_row(a.Y + t * a.ldy + c + 32 * hw, v, have);
+                        // Past the L2 where the residual's rows go through it too: 25728 x 1024 ->
+                        // 4096 194 us without, 177 with, 25728 x 4096 -> 1024 115 and 110.  Without a
+                        // residual it is 1 to 3 % either way: a tile waits longer for its stores.
+                        store_row<SCALED && RESIDUAL && ACT >= 0>(a.Y + t * a.ldy + c + 32 * hw, v, have);
                     }
                 }
                 if constexpr (SCALED) __builtin_amdgcn_sched_barrier(0);

@@ -56,7 +56,11 @@ template <int THREADS> __device__ __forceinline__ RowStats joined_row(RowStats v
     return v;
 }
 
-// V elements as they lie in memory (16 bytes), any alignment of their type.
+// V elements as they lie in memory (16 bytes), any alignment of their type.  Results are
+// stored non-temporally: they do not push out of the L2 what other workgroups are about to
+// read (16384 x 4096 bf16, norm with residual to 8 bits 81.5 us without, 76.2 with, to bf16 91
+// and 85, dequantisation 33.7 and 29.5).  Loads of that kind gain less and cost a few us where X
+// still lies in a cache.
 template <typename E> struct Chunk {
     static constexpr int V = 16 / (int)sizeof(E);
     union {
@@ -64,7 +68,7 @@ template <typename E> struct Chunk {
         E e[V];
     };
     __device__ __forceinline__ void load(const E *p) { u = *reinterpret_cast<const u32x4_any *>(p); }
-    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<u32x4_any *>(p) = u; }
+    __device__ __forceinline__ void store(E *p) const { __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(p)); }
 };
 
 // The whole number nearest to y * steps (|y * steps| < 2^21) in the low bits: added to
@@ -81,8 +85,9 @@ template <int V> __device__ __forceinline__ void store_bytes(i8 *p, const unsign
     typedef unsigned u32_any __attribute__((aligned(1)));
     typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
     typedef u32x2 u32x2_any __attribute__((aligned(1)));
-    if constexpr (V == 4) *reinterpret_cast<u32_any *>(p) = bytes4(q[0], q[1], q[2], q[3]);
-    else *reinterpret_cast<u32x2_any *>(p) = u32x2{bytes4(q[0], q[1], q[2], q[3]), bytes4(q[4], q[5], q[6], q[7])};
+    const unsigned lo = bytes4(q[0], q[1], q[2], q[3]);
+    if constexpr (V == 4) __builtin_nontemporal_store(lo, reinterpret_cast<u32_any *>(p));
+    else __builtin_nontemporal_store(u32x2{lo, bytes4(q[4], q[5], q[6], q[7])}, reinterpret_cast<u32x2_any *>(p));
 }
 
 // Threads of a workgroup: rows within a wavefront share one, longer rows have their own.
@@ -90,9 +95,9 @@ constexpr int rows_threads(int row) { return row <= 64 ? 256 : row; }
 
 // THREADS threads hold a row of up to THREADS * CHUNKS whole 16-byte chunks, and one
 // more element each of the rest: it is read once, all its loads in flight together.  Bound
-// by memory: 16384 x 4096 bf16 with residual 81.5 us to 8 bits (5.8 TB/s of read and
-// written bytes) and 95 to bf16 (5.7); quantisation 34 us (5.9), 16384 x 14336 128 (5.5).
-// One workgroup a row that was read twice, by elements: 255, 105 at 25728 x 1024 (39), 330.
+// by memory: 16384 x 4096 bf16 with residual 76 us to 8 bits (6.2 TB/s of read and
+// written bytes) and 89 to bf16 (6.0); quantisation 34 us (5.9), 16384 x 14336 121 (5.8).
+// One workgroup a row that was read twice, by elements: 255, 105 at 25728 x 1024 (37), 330.
 template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
 __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> a) {
     constexpr int V = Chunk<E>::V, ROWS = rows_threads(THREADS) / THREADS;

@@ -94,16 +94,17 @@ constexpr int kRingBytes = 16384;  // of LDS for each wavefront's ring
 // weights and XROWS of tokens a slab (16 or 8 each, XROWS also 0 or 32; with 8, rows
 // 8 .. 15 of the fragments repeat them, with 32 there are two fragments of 16).  The
 // tokens' rows may lie anywhere: their slab is at byte `kx` of them.
-template <typename E, int WROWS, int XROWS> struct SlabRing {
+// ONCE: the weights' slabs are read once.
+template <typename E, int WROWS, int XROWS, bool ONCE = false> struct SlabRing {
     static constexpr int WBYTES = 128 * WROWS, SLAB = WBYTES + 128 * XROWS;
     static constexpr int DEPTH = kRingBytes / SLAB, COPIES = (WROWS + XROWS) / 8;
     char *ring;            // this wavefront's kRingBytes of LDS
     int at = 0;            // place of the oldest slab, and of the next to issue
 
-    template <int ROWS> __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
+    template <int ROWS, bool LAST> __device__ __forceinline__ void copy(const SlabRows &r, uint32_t k, int left, char *dst) {
 #pragma unroll
         for (int q = 0; q < ROWS / 8; ++q)
-            buffer_to_lds16(r.buf[q], (int)slab_chunk() < left ? r.off[q] : kOutside, k, dst + 1024 * q);
+            buffer_to_lds16<LAST>(r.buf[q], (int)slab_chunk() < left ? r.off[q] : kOutside, k, dst + 1024 * q);
     }
     // Copies one slab at byte `k` of the rows; `left` bytes of the rows are left.
     __device__ __forceinline__ void issue(const SlabRows &w, uint32_t k, int left) { issue(w, w, k, left); }
@@ -114,9 +115,9 @@ template <typename E, int WROWS, int XROWS> struct SlabRing {
                                           int left) {
         char *dst = ring + at * SLAB;
         if (left <= 0) k = kx = 0;  // past a short buffer's end the range check could wrap
-        copy<WROWS>(w, k, left, dst);
-        if constexpr (XROWS > 0) copy<(XROWS < 16 ? XROWS : 16)>(x, kx, left, dst + WBYTES);
-        if constexpr (XROWS == 32) copy<16>(x2, kx, left, dst + WBYTES + 16 * 128);
+        copy<WROWS, ONCE>(w, k, left, dst);
+        if constexpr (XROWS > 0) copy<(XROWS < 16 ? XROWS : 16), false>(x, kx, left, dst + WBYTES);
+        if constexpr (XROWS == 32) copy<16, false>(x2, kx, left, dst + WBYTES + 16 * 128);
         at = at + 1 == DEPTH ? 0 : at + 1;
     }
     // Waits for the oldest slab and reads its fragments; the next issue has to
@@ -203,7 +204,7 @@ __device__ __forceinline__ void stream_products(const Position &start, int row_b
     asm volatile("" ::: "memory");
 
     // the stream of weights: slabs s0 .. s1 of position after position
-    SlabRing<E, 16, 0> ring{lds.ring + wave * kRingBytes};
+    SlabRing<E, 16, 0, sizeof(E) == 1> ring{lds.ring + wave * kRingBytes};
     SlabRows w;
     Position in = start;
     int in_slab = s0;

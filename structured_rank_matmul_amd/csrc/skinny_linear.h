@@ -99,7 +99,8 @@ __global__ __launch_bounds__(kThreads) void skinny_kernel(LinearArgs<E, O> a, in
     stream_products<E, SLABS, TB>(start, (int)(a.K * (int)sizeof(E)), lds);
 }
 
-template <typename E, typename O, class U_>
+// ONCE: of 8-bit operands, one group: no slab of the units is read again.
+template <typename E, typename O, class U_, bool ONCE = false>
 __global__ __launch_bounds__(kThreads) void skinny_ring_kernel(LinearArgs<E, O> a, int units, int groups) {
     __shared__ __align__(16) StreamLds<1> lds;
     const U_ U{&a};
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void skinny_ring_kernel(LinearArgs<E, O> 
     const int s0 = min(slabs, wave * per), s1 = min(slabs, s0 + per);  // this wavefront's slabs
 
     // the stream: slabs s0 .. s1 of segment after segment (unit, token group)
-    SlabRing<E, 16, 16> ring{lds.ring + wave * kRingBytes};
+    SlabRing<E, 16, 16, ONCE> ring{lds.ring + wave * kRingBytes};
     SlabRows w, x;
     const uint32_t xld = (uint32_t)(U.other_ld() * sizeof(E));
 #pragma unroll
@@ -227,6 +228,11 @@ template <typename E, typename O, bool GATED> hipError_t launch_skinny(const Lin
         case 8: return launch_slabs<E, O, GATED, 8, 2>(a, units, st);
         case 12: return launch_slabs<E, O, GATED, 12, 2>(a, units, st);
         }
+    }
+    if (sizeof(E) == 1 && a.M <= 16) {
+        hipLaunchKernelGGL((skinny_ring_kernel<E, O, Units<E, O, GATED>, sizeof(E) == 1>), dim3(workgroups(units)),
+                           dim3(kThreads), 0, st, a, units, 1);
+        return hipGetLastError();
     }
     hipLaunchKernelGGL((skinny_ring_kernel<E, O, Units<E, O, GATED>>), dim3(workgroups(units)), dim3(kThreads), 0, st, a,
                        units, (int)((a.M + 15) / 16));

@@ -574,18 +574,25 @@ def dyra_gated(X, Wg, Wu, bias_g=None, bias_u=None, act: str = "silu", H=None, s
 
 
 def _types():
-    """(torch.int8, torch.float32, torch.bfloat16)"""
+    """(torch.int8, torch.float32, torch.bfloat16, torch.empty_like)"""
     global _torch_types
     if _torch_types is None:
         import torch
-        _torch_types = (torch.int8, torch.float32, torch.bfloat16)
+        _torch_types = (torch.int8, torch.float32, torch.bfloat16, torch.empty_like)
     return _torch_types
 
 
 _torch_types = None
 
 
-def _norm_inputs(X, N, c, dev, weight, residual, S, stream):
+def _rows_like(X, N, c, ldx, dtype, stream):
+    """A new [N, c] matrix beside X of that shape."""
+    if stream is not None or ldx != c:
+        return _new((N, c), dtype, X, stream)
+    return _types()[3](X, dtype=dtype)   # 0.3 us less than new_empty
+
+
+def _norm_inputs(X, N, c, ldx, dev, weight, residual, S, stream):
     """(weight, residual, its row stride, S tensor, its address, its row stride) of the norms."""
     t = X.dtype
     w = None if weight is None else _whole(weight, "weight", dev, (c,), t)
@@ -595,7 +602,7 @@ def _norm_inputs(X, N, c, dev, weight, residual, S, stream):
         return w, None, 0, None, None, 0
     r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c, t, True)
     if S is None:
-        S, lds = _new((N, c), t, X, stream), c
+        S, lds = _rows_like(X, N, c, ldx, t, stream), c
     else:
         lds = _matrix(S, "S", dev, N, c, t)
     return w, r, ldr, S, S.data_ptr(), lds
@@ -610,9 +617,9 @@ def dyra_norm(X, weight=None, eps: float = 1e-6, residual=None, S=None, Y=None, 
         return _with_device(dev, dyra_norm, X, weight, eps, residual, S, Y, stream)
     t = X.dtype
     code = _codes[t]
-    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, dev, weight, residual, S, stream)
+    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, ldx, dev, weight, residual, S, stream)
     if Y is None:
-        Y, ldy = _new((N, c), t, X, stream), c
+        Y, ldy = _rows_like(X, N, c, ldx, t, stream), c
     else:
         ldy = _matrix(Y, "Y", dev, N, c, t)
     status = (_lib or load()).dyra_norm(X.data_ptr(), ldx, N, c, code, r, ldr, w, eps, s, lds, Y.data_ptr(), ldy, st)
@@ -621,15 +628,15 @@ def dyra_norm(X, weight=None, eps: float = 1e-6, residual=None, S=None, Y=None, 
     return Y if S is None else (Y, S)
 
 
-def _eight_bits(X, N, c, dev, Q, scales, stream):
+def _eight_bits(X, N, c, ldx, dev, Q, scales, stream):
     """(Q, its row stride, scales) to be written."""
-    i8, f32, _ = _types()
+    i8, f32, *_ = _types()
     if Q is None:
-        Q, ldq = _new((N, c), i8, X, stream), c
+        Q, ldq = _rows_like(X, N, c, ldx, i8, stream), c
     else:
         ldq = _matrix(Q, "Q", dev, N, c, i8)
     if scales is None:
-        scales = _new((N,), f32, X, stream)
+        scales = X.new_empty(N, dtype=f32) if stream is None else _new((N,), f32, X, stream)
     else:
         _whole(scales, "scales", dev, (N,), f32)
     return Q, ldq, scales
@@ -642,8 +649,8 @@ def dyra_norm_quantize(X, weight=None, eps: float = 1e-6, residual=None, S=None,
     if st is None:
         return _with_device(dev, dyra_norm_quantize, X, weight, eps, residual, S, Q, scales, stream)
     code = _codes[X.dtype]
-    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, dev, weight, residual, S, stream)
-    Q, ldq, scales = _eight_bits(X, N, c, dev, Q, scales, stream)
+    w, r, ldr, S, s, lds = _norm_inputs(X, N, c, ldx, dev, weight, residual, S, stream)
+    Q, ldq, scales = _eight_bits(X, N, c, ldx, dev, Q, scales, stream)
     status = (_lib or load()).dyra_norm_quantize(X.data_ptr(), ldx, N, c, code, r, ldr, w, eps, s, lds, Q.data_ptr(), ldq,
                                                  scales.data_ptr(), st)
     if status != 0:
@@ -659,7 +666,7 @@ def dyra_quantize(X, Q=None, scales=None, stream=None):
     if st is None:
         return _with_device(dev, dyra_quantize, X, Q, scales, stream)
     code = _codes[X.dtype]
-    Q, ldq, scales = _eight_bits(X, N, c, dev, Q, scales, stream)
+    Q, ldq, scales = _eight_bits(X, N, c, ldx, dev, Q, scales, stream)
     status = (_lib or load()).dyra_quantize(X.data_ptr(), ldx, N, c, code, Q.data_ptr(), ldq, scales.data_ptr(), st)
     if status != 0:
         raise DyraError(status, "dyra_quantize")
@@ -672,14 +679,14 @@ def dyra_dequantize(Q, scales, out_dtype=None, X=None, stream=None):
     st = _stream_on(dev, stream)
     if st is None:
         return _with_device(dev, dyra_dequantize, Q, scales, out_dtype, X, stream)
-    i8, f32, bf16 = _types()
+    i8, f32, bf16, _ = _types()
     if Q.dtype != i8:
         raise ValueError(f"Q must be int8, got {Q.dtype}")
     s = _whole(scales, "scales", dev, (N,), f32)
     out = bf16 if out_dtype is None else out_dtype
     code = _codes[out]
     if X is None:
-        X, ldx = _new((N, c), out, Q, stream), c
+        X, ldx = _rows_like(Q, N, c, ldq, out, stream), c
     else:
         ldx = _matrix(X, "X", dev, N, c, out)
     status = (_lib or load()).dyra_dequantize(Q.data_ptr(), ldq, s, N, c, code, X.data_ptr(), ldx, st)
@@ -723,7 +730,7 @@ def dyra_linear_quantized(X, x_scales, Wt, w_scales, bias=None, act: str = "none
     if st is None:
         return _with_device(dev, dyra_linear_quantized, X, x_scales, Wt, w_scales, bias, act, residual, out_dtype, Y, workspace,
                             stream)
-    i8, f32, bf16 = _types()
+    i8, f32, bf16, _ = _types()
     if X.dtype != i8:
         raise ValueError(f"X must be int8, got {X.dtype}")
     c2 = Wt.shape[0]
@@ -737,7 +744,7 @@ def dyra_linear_quantized(X, x_scales, Wt, w_scales, bias=None, act: str = "none
         r, ldr = residual.data_ptr(), _matrix(residual, "residual", dev, N, c2, out, True)
     acode = _ACTS[act]
     if Y is None:
-        Y, ldy = _new((N, c2), out, X, stream), c2
+        Y, ldy = X.new_empty(N, c2, dtype=out) if stream is None else _new((N, c2), out, X, stream), c2
     else:
         ldy = _matrix(Y, "Y", dev, N, c2, out)
     workspace, wp, size = _split_workspace(workspace, X, dev, N, c1, c2, False, stream)
@@ -757,7 +764,7 @@ def dyra_gated_quantized(X, x_scales, Wg, g_scales, Wu, u_scales, bias_g=None, b
     if st is None:
         return _with_device(dev, dyra_gated_quantized, X, x_scales, Wg, g_scales, Wu, u_scales, bias_g, bias_u, act, out_dtype,
                             H, workspace, stream)
-    i8, f32, bf16 = _types()
+    i8, f32, bf16, _ = _types()
     if X.dtype != i8:
         raise ValueError(f"X must be int8, got {X.dtype}")
     c2 = Wg.shape[0]
@@ -772,7 +779,7 @@ def dyra_gated_quantized(X, x_scales, Wg, g_scales, Wu, u_scales, bias_g=None, b
     bu = None if bias_u is None else _whole(bias_u, "bias_u", dev, (c2,), out)
     acode = _ACTS[act]
     if H is None:
-        H, ldh = _new((N, c2), out, X, stream), c2
+        H, ldh = X.new_empty(N, c2, dtype=out) if stream is None else _new((N, c2), out, X, stream), c2
     else:
         ldh = _matrix(H, "H", dev, N, c2, out)
     workspace, wp, size = _split_workspace(workspace, X, dev, N, c1, c2, True, stream)

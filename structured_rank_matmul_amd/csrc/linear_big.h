@@ -38,10 +38,9 @@
 #pragma once
 
 #include "ffn_tile.h"
+#include "linear_scaled.h"
 
 namespace dyra {
-
-template <int N> using ic = std::integral_constant<int, N>;
 
 // The lane number, computed anew: what is derived from it is not kept in
 // registers across the main loop (whose accumulators and fragments need them).
@@ -49,12 +48,6 @@ __device__ __forceinline__ int fresh_lane() {
     int l = threadIdx.x & 63;
     asm volatile("" : "+v"(l));
     return l;
-}
-
-__device__ __forceinline__ unsigned bits_of(bf16 v) { return __builtin_bit_cast(unsigned short, v); }
-__device__ __forceinline__ unsigned bits_of(float v) { return __builtin_bit_cast(unsigned, v); }
-template <typename T> __device__ __forceinline__ float value_of(unsigned bits) {
-    return __builtin_bit_cast(float, sizeof(T) == 2 ? bits << 16 : bits);
 }
 
 template <typename E, typename O, bool GATED, int TB>
@@ -232,23 +225,10 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
     wait_lds_and_vm<8>();
     barrier_only();
     if (wm == 1) barrier_only();
-    typedef typename LinearArgs<E, O>::Bias Bias;
     for (;;) {
-        // 8-bit operands: lane l loads the scale and the bias of the wavefront's weight row l, and
-        // the scales of its tokens l and 64 + l, which the tile's products leave time to arrive.
-        // Loaded in the epilogue, one after the other, they cost it 2 us a tile.
-        float scale_w = 0.f, scale_x[2] = {};
-        unsigned bias_bits = 0;
+        std::conditional_t<SCALED, TileScales<O, GATED>, ic<0>> scales;
         if constexpr (SCALED) {
-            const int l = fresh_lane();
-            const bool up = GATED && l >= 32;
-            const unsigned f = (unsigned)min((int)col0 + (GATED ? 32 * wn + (l & 31) : 64 * wn + l), (int)a.N - 1);
-            scale_w = (up ? a.scale.w1 : a.scale.w0)[f];
-            const Bias *const b = up ? a.b1 : a.b0;
-            if (b) bias_bits = bits_of(b[f]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                scale_x[h] = a.scale.x[(unsigned)min((int)row0 + 16 * TB * wm + 64 * h + l, (int)a.M - 1)];
+            scales.load(a, (int)row0 + 16 * TB * wm, (int)col0 + (GATED ? 32 : 64) * wn, fresh_lane());
             __builtin_assume(slabs > 0);  // no way past the products, on which the loads would be waited for
         }
 #pragma unroll
@@ -271,93 +251,54 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
         const int el = fresh_lane(), ei = el & 15, eg = el >> 4;
         const bool whole = row0 + BM <= a.M && col0 + BF <= a.N;
         stores_out = whole;
+        if constexpr (SCALED) {
+            scaled_epilogue<TB>(a, acc, scales, reinterpret_cast<float *>(smem + 4 * STAGE) + 256 * wave, row0 + 16 * TB * wm,
+                                col0 + (GATED ? 32 : 64) * wn, el, whole);
+        } else {
         constexpr int HW = GATED ? 1 : 2;
         const int64_t c = col0 + (GATED ? 32 : 64) * wn + 8 * eg;  // hw = 1: 32 on
         float b0[HW][8] = {}, b1[8] = {};
-        if constexpr (!SCALED) {
 #pragma unroll
-            for (int hw = 0; hw < HW; ++hw)
-                if (a.b0) load_row(a.b0 + c + 32 * hw, b0[hw], whole ? 8 : (int)(a.N - c) - 32 * hw);
-            if (GATED && a.b1) load_row(a.b1 + c, b1, whole ? 8 : (int)(a.N - c));
-        }
-        // Results before the activation, in the sums' registers.  Those of 8-bit operands are
-        // all made here: left to the activations' copies of the code, the compiler made them
-        // ahead of the branch all the same, and kept 46 to 172 registers in scratch.
-        f32x4 z[2][2][4][2];
-        if constexpr (SCALED) {
-            float *const mine = reinterpret_cast<float *>(smem + 4 * STAGE) + 256 * wave;
-            asm volatile("" : "+v"(bias_bits));  // no conversion, and no wait for it, ahead of the products
-            mine[el] = scale_w;
-            mine[64 + el] = value_of<Bias>(bias_bits);
-            mine[128 + el] = scale_x[0];
-            mine[192 + el] = scale_x[1];
-            float sx[TB];
-#pragma unroll
-            for (int i = 0; i < TB; ++i) sx[i] = mine[128 + 16 * i + ei];
-#pragma unroll
-            for (int hw = 0; hw < 2; ++hw)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const f32x4 sw = *reinterpret_cast<const f32x4 *>(mine + 32 * hw + 8 * eg + 4 * j);
-                    const f32x4 b = *reinterpret_cast<const f32x4 *>(mine + 64 + 32 * hw + 8 * eg + 4 * j);
-#pragma unroll
-                    for (int i = 0; i < TB; ++i) {
-                        f32x4 &v = z[i >> 2][hw][i & 3][j];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = biased(acc[i >> 2][hw][i & 3][j][q], sx[i], sw[q], b[q]);
-                        asm volatile("" : "+v"(v));
-                    }
-                }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        auto result = [&](int i, int hw, int q) __attribute__((always_inline)) {
-            if constexpr (SCALED) return z[i >> 2][hw][i & 3][q >> 2][q & 3];
-            else return acc[i >> 2][hw][i & 3][q >> 2][q & 3] + (GATED && hw ? b1[q] : b0[GATED ? 0 : hw][q]);
-        };
+        for (int hw = 0; hw < HW; ++hw)
+            if (a.b0) load_row(a.b0 + c + 32 * hw, b0[hw], whole ? 8 : (int)(a.N - c) - 32 * hw);
+        if (GATED && a.b1) load_row(a.b1 + c, b1, whole ? 8 : (int)(a.N - c));
         // ACT below 0: of the call, with guards
         auto finish = [&](auto act, auto residual) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
             constexpr bool RESIDUAL = decltype(residual)::value;
             // rows whose residual is in flight together: what registers allow
-            constexpr int FIT = (TB == 8 ? 2 : 4) * 2 / (int)sizeof(O);
-            constexpr int BATCH = RESIDUAL && ACT >= 0 ? (SCALED && ACT == kActGelu && FIT > 1 ? FIT / 2 : FIT) : 1;
+            constexpr int BATCH = RESIDUAL && ACT >= 0 ? (TB == 8 ? 2 : 4) * 2 / (int)sizeof(O) : 1;
             const int64_t first = row0 + 16 * TB * wm + ei;
             // both halves of a row one after the other: whole 128-byte lines
 #pragma unroll
             for (int i0 = 0; i0 < TB; i0 += BATCH) {
-                int64_t row = first + 16 * i0;
-                if constexpr (SCALED) asm volatile("" : "+v"(row));  // no addresses of later rows are held
                 Residual8<O> r[BATCH][HW];
                 if constexpr (RESIDUAL && ACT >= 0) {
 #pragma unroll
                     for (int i = i0; i < i0 + BATCH && i < TB; ++i)
 #pragma unroll
-                        for (int hw = 0; hw < HW; ++hw) r[i - i0][hw].request(a.R + (row + 16 * (i - i0)) * a.ldr + c + 32 * hw);
+                        for (int hw = 0; hw < HW; ++hw) r[i - i0][hw].request(a.R + (first + 16 * i) * a.ldr + c + 32 * hw);
                 }
 #pragma unroll
                 for (int i = i0; i < i0 + BATCH && i < TB; ++i) {
-                    const int64_t t = row + 16 * (i - i0);
+                    const int64_t t = first + 16 * i;
                     if (ACT < 0 && t >= a.M) continue;
 #pragma unroll
                     for (int hw = 0; hw < HW; ++hw) {
                         const int have = ACT >= 0 ? 8 : (int)max((int64_t)0, min((int64_t)8, a.N - c - 32 * hw));
                         float v[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] = result(i, hw, q);
+                        for (int q = 0; q < 8; ++q) v[q] = acc[i >> 2][hw][i & 3][q >> 2][q & 3] + b0[hw][q];
                         activate<sizeof(O) == 4>(v, ACT >= 0 ? ACT : a.act);
                         if constexpr (GATED) {
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) v[q] *= result(i, 1, q);
+                            for (int q = 0; q < 8; ++q) v[q] *= acc[i >> 2][1][i & 3][q >> 2][q & 3] + b1[q];
                         }
                         if constexpr (RESIDUAL && ACT >= 0) r[i - i0][hw].add_to(v);
                         else if constexpr (RESIDUAL) add_row(v, a.R + t * a.ldr + c + 32 * hw, have);
-                        // Past the L2 where the residual's rows go through it too: 25728 x 1024 ->
-                        // 4096 194 us without, 177 with, 25728 x 4096 -> 1024 115 and 110.  Without a
-                        // residual it is 1 to 3 % either way: a tile waits longer for its stores.
-                        store_row<SCALED && RESIDUAL && ACT >= 0>(a.Y + t * a.ldy + c + 32 * hw, v, have);
+                        store_row(a.Y + t * a.ldy + c + 32 * hw, v, have);
                     }
                 }
-                if constexpr (SCALED) __builtin_amdgcn_sched_barrier(0);
             }
         };
         auto finish_act = [&](auto act) __attribute__((always_inline)) {
@@ -372,6 +313,7 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
         else if (a.act == kActGelu) finish_act(ic<kActGelu>{});
         else if (a.act == kActGeluTanh) finish_act(ic<kActGeluTanh>{});
         else finish_act(ic<kActSilu>{});
+        }
         tile += nslots;
         if (tile >= band_end) break;
         row0 = next_row0;

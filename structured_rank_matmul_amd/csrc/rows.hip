@@ -13,6 +13,7 @@
 // the same up to eps 2^-192, which is nothing beside them.
 #include "ffn_tile.h"
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -21,6 +22,8 @@ namespace dyra {
 namespace {
 
 constexpr float kLeastTop = 127.f * FLT_MIN;
+// Threads of a launch along its first dimension: below 2^32.  More rows take more launches.
+constexpr int64_t kLaunchThreads = int64_t{1} << 31;
 
 // What a row's threads find together: the sum of squares, and the largest magnitude as
 // its bits, which order as the magnitudes do with NaN above infinity.
@@ -212,7 +215,6 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         if (last) y[rest] = (i8)(finite ? nearest(z1 * by * w1 * rho, steps) : 0u);
     } else {
         E *const y = (E *)a.Y + row * a.ldy;
-        const float by_rho = by * rho;  // of a row that is summed again, at least 2^-96 / (2^32 sqrt c)
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int k = t + i * THREADS;
@@ -220,11 +222,11 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
             if (k < chunks) {
                 Chunk<E> o;
 #pragma unroll
-                for (int q = 0; q < V; ++q) o.e[q] = to_elem<E>(z[i][q] * by_rho * weight(i, q));
+                for (int q = 0; q < V; ++q) o.e[q] = to_elem<E>(z[i][q] * by * rho * weight(i, q));
                 o.store(y + k * V);
             }
         }
-        if (last) y[rest] = to_elem<E>(z1 * by_rho * w1);
+        if (last) y[rest] = to_elem<E>(z1 * by * rho * w1);
     }
 }
 
@@ -257,11 +259,23 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const i8 *Q, int64_t ld
 }
 
 template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
-hipError_t launch_held(const RowArgs<E> &a, hipStream_t st) {
+hipError_t launch_held(RowArgs<E> a, hipStream_t st) {
     constexpr int ROWS = rows_threads(THREADS) / THREADS;
-    hipLaunchKernelGGL((rows_kernel<E, NORM, EIGHT, THREADS, CHUNKS>), dim3((unsigned)((a.N + ROWS - 1) / ROWS)),
-                       dim3(rows_threads(THREADS)), 0, st, a);
-    return hipGetLastError();
+    constexpr int64_t MOST = kLaunchThreads / THREADS;  // rows of a launch
+    typedef std::conditional_t<EIGHT, i8, E> Out;
+    for (int64_t left = a.N; left > 0; left -= MOST) {
+        a.N = std::min(left, MOST);
+        hipLaunchKernelGGL((rows_kernel<E, NORM, EIGHT, THREADS, CHUNKS>), dim3((unsigned)((a.N + ROWS - 1) / ROWS)),
+                           dim3(rows_threads(THREADS)), 0, st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || left <= MOST) return e;
+        a.X += MOST * a.ldx;
+        if (a.R) a.R += MOST * a.ldr;
+        if (a.S) a.S += MOST * a.lds;
+        a.Y = (Out *)a.Y + MOST * a.ldy;
+        if (EIGHT) a.scales += MOST;
+    }
+    return hipSuccess;
 }
 // Two chunks a thread while that gives threads enough: more loads in flight than with one,
 // more threads than with four.  us by threads x chunks of a row, norm with residual to 8
@@ -290,10 +304,16 @@ template <typename E, bool NORM, bool EIGHT> hipError_t launch_rows(const RowArg
 template <typename E, int THREADS>
 hipError_t launch_back(const i8 *Q, int64_t ldq, const float *scales, int64_t N, int64_t c, E *X, int64_t ldx, hipStream_t st) {
     constexpr int ROWS = 256 / THREADS, PIECE = Chunk<E>::V * THREADS;
-    hipLaunchKernelGGL((dequantize_kernel<E, THREADS>),
-                       dim3((unsigned)((N + ROWS - 1) / ROWS), (unsigned)((c + PIECE - 1) / PIECE)), dim3(256), 0, st, Q, ldq,
-                       scales, N, (int)c, X, ldx);
-    return hipGetLastError();
+    constexpr int64_t MOST = kLaunchThreads / THREADS;
+    for (int64_t from = 0; from < N; from += MOST) {
+        const int64_t rows = std::min(N - from, MOST);
+        hipLaunchKernelGGL((dequantize_kernel<E, THREADS>),
+                           dim3((unsigned)((rows + ROWS - 1) / ROWS), (unsigned)((c + PIECE - 1) / PIECE)), dim3(256), 0, st,
+                           Q + from * ldq, ldq, scales + from, rows, (int)c, X + from * ldx, ldx);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -593,3 +593,28 @@ def test_binding_refuses_mismatched_tensors():
         with pytest.raises(dyra.DyraError) as err:
             call()
         assert err.value.status == status
+
+
+def test_more_rows_than_a_launch_has_threads_for():
+    """2^24 rows and more of 256 threads each: several launches, of which the rows around the joins and the last are checked.
+    The norm in place, so that its rows are read and written where a wrong offset would show."""
+    import torch
+    t, c = torch.bfloat16, 2056
+    N, joins = (1 << 24) + 70, [1 << 23, 1 << 24]     # 2^31 / 256 rows a launch
+    x = torch.empty(N, c, dtype=t, device="cuda")
+    at = [slice(0, 20)] + [slice(j - 20, j + 20) for j in joins] + [slice(N - 20, N)]
+    rows = [rand((x[s].shape[0], c), 120 + i, t) for i, s in enumerate(at)]
+    for s, r in zip(at, rows):
+        x[s] = r.cuda()
+    w = rand((c,), 130, t)
+    q, scales = dyra.dyra_quantize(x)
+    for s, r in zip(at, rows):
+        check_rows(q[s], scales[s], r.double(), False)
+    out = dyra.dyra_norm(x, w.cuda(), EPS, Y=x)
+    assert out is x
+    for s, r in zip(at, rows):
+        check_norm(x[s], norm_ref(r, w, EPS, None)[1], c)
+    dyra.dyra_dequantize(q, scales, X=x)
+    for s in at:
+        v = q[s].cpu().double() * scales[s].cpu().double()[:, None]
+        close(x[s], v, (U + half(t)) * v.abs() * 1.01)

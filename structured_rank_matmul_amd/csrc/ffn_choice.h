@@ -107,6 +107,7 @@ inline Split pick_split(bool gated, int64_t M, int64_t N, int64_t row_bytes) {
     const Tile whole = pick_tile(1, gated, M, N, row_bytes);
     const double count = std::ceil((double)M / kTiles[whole].bm) * std::ceil(rows / kTiles[whole].bn);
     Split best{whole, 1, (int)slabs};
+    if (whole > T128x256) return best;  // tiles enough; and a gelu that does not depend on the workspace (gelu_table.h)
     double cost = 0.9 * std::ceil(count / 256.0) * (slabs * kTiles[whole].slab * (whole <= T128x128 ? 1.5 : 1.0) + kTiles[whole].once);
     for (int i = T64x64; i <= T128x256; ++i) {
         const TileCost &t = kTiles[i];

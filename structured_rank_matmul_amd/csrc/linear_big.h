@@ -61,7 +61,9 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
     constexpr int STORES = (GATED ? 1 : 2) * TB * (8 * (int)sizeof(O) / 16);
     // 8-bit operands: behind them, each wavefront's scales and biases in the epilogue
     constexpr bool SCALED = sizeof(E) == 1;
-    __shared__ __align__(16) char smem[4 * STAGE + (SCALED ? 8 * 1024 : 0)];
+    constexpr bool TABLE = SCALED && sizeof(O) == 2;
+    __shared__ __align__(16) char smem[4 * STAGE + (SCALED ? 8 * 512 : 0) + (TABLE ? (int)sizeof(GeluTable) : 0)];
+    constexpr int SCALES_AT = 4 * STAGE + (TABLE ? (int)sizeof(GeluTable) : 0);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
@@ -211,6 +213,9 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
     next_row0 = row0;
     next_col0 = col0;
     sources(row0, col0);
+    if constexpr (TABLE) {
+        if (a.act == kActGelu) copy_gelu_table(smem + 4 * STAGE, wave, lane);  // older than the slabs: lands before them
+    }
     copy_w(0, 0);
     copy_x(0, 0);
     copy_w(1, 0);
@@ -252,8 +257,8 @@ __global__ __launch_bounds__(512, 2) void linear_big_kernel(LinearArgs<E, O> a, 
         const bool whole = row0 + BM <= a.M && col0 + BF <= a.N;
         stores_out = whole;
         if constexpr (SCALED) {
-            scaled_epilogue<TB>(a, acc, scales, reinterpret_cast<float *>(smem + 4 * STAGE) + 256 * wave, row0 + 16 * TB * wm,
-                                col0 + (GATED ? 32 : 64) * wn, el, whole);
+            scaled_epilogue<TB>(a, acc, scales, reinterpret_cast<float *>(smem + SCALES_AT) + 128 * wave, smem + 4 * STAGE,
+                                row0 + 16 * TB * wm, col0 + (GATED ? 32 : 64) * wn, el, whole);
         } else {
         constexpr int HW = GATED ? 1 : 2;
         const int64_t c = col0 + (GATED ? 32 : 64) * wn + 8 * eg;  // hw = 1: 32 on

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "ffn_tile.h"
+#include "gelu_table.h"
 
 namespace dyra {
 
@@ -34,26 +35,50 @@ template <typename O, bool GATED> struct TileScales {
     }
 };
 
-// The epilogue.  `row` and `col` as above, `el` the lane, `mine` 1 KB of LDS of the wavefront;
-// `whole`: no token or feature lies past the end.
+// The epilogue.  `row` and `col` as above, `el` the lane, `mine` 512 bytes of LDS of the wavefront,
+// `table` the workgroup's GeluTable (bf16 results with kActGelu); `whole`: no token or feature
+// lies past the end.
 template <int TB, bool GATED, typename O>
 __device__ __forceinline__ void scaled_epilogue(const LinearArgs<i8, O> &a, const i32x4 (&acc)[2][2][4][2], TileScales<O, GATED> s,
-                                                float *mine, int64_t row0, int64_t col0, int el, bool whole) {
+                                                float *mine, const char *table, int64_t row0, int64_t col0, int el, bool whole) {
     constexpr int HW = GATED ? 1 : 2;
     const int ei = el & 15, eg = el >> 4;
     const int64_t c = col0 + 8 * eg;  // hw = 1: 32 on
+    // Rows whose residual is in flight together: what registers allow.  A row's is asked for
+    // before the row FIT ahead of it is stored, as a wait for loads waits for older stores, and
+    // the first ones before the sums are scaled, where that spills no registers.  us, FIT rows
+    // at a time | this: 25728 x 1024 -> 4096 173 | 163, with GELU 178 | 171, 25728 x 4096 -> 1024
+    // 111 | 109, 16384 x 14336 -> 4096 704 | 694.
+    constexpr int FIT = (TB == 8 ? 2 : 4) * 2 / (int)sizeof(O);
+    constexpr bool EARLY = TB < 8;
+    const int64_t first = row0 + ei, step = 16 * a.ldy, step_r = 16 * a.ldr;
+    Residual8<O> res[FIT][HW];
+    int64_t at_r = 0;
+    auto request = [&](int i) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(at_r));  // no addresses of later rows are held
+#pragma unroll
+        for (int hw = 0; hw < HW; ++hw) res[i % FIT][hw].request(a.R + at_r + 32 * hw);
+        at_r += step_r;
+    };
+    auto request_first = [&]() __attribute__((always_inline)) {
+        at_r = first * a.ldr + c;
+#pragma unroll
+        for (int i = 0; i < FIT; ++i) request(i);
+    };
+    if (!GATED && EARLY && whole && a.R) request_first();
     // Results before the activation, in the sums' registers, all made here: left to the
     // activations' copies of the code, the compiler made them ahead of the branch all the
     // same, and kept 46 to 172 registers in scratch.
     f32x4 z[2][2][4][2];
     asm volatile("" : "+v"(s.bias));  // no conversion, and no wait for it, ahead of the products
-    mine[el] = s.w;
-    mine[64 + el] = value_of<O>(s.bias);
-    mine[128 + el] = s.x[0];
-    mine[192 + el] = s.x[1];
+    mine[el] = s.x[0];
+    mine[64 + el] = s.x[1];
     float sx[TB];
 #pragma unroll
-    for (int i = 0; i < TB; ++i) sx[i] = mine[128 + 16 * i + ei];
+    for (int i = 0; i < TB; ++i) sx[i] = mine[16 * i + ei];
+    __builtin_amdgcn_wave_barrier();
+    mine[el] = s.w;  // a wavefront's LDS accesses are in order
+    mine[64 + el] = value_of<O>(s.bias);
 #pragma unroll
     for (int hw = 0; hw < 2; ++hw)
 #pragma unroll
@@ -73,46 +98,43 @@ __device__ __forceinline__ void scaled_epilogue(const LinearArgs<i8, O> &a, cons
     auto finish = [&](auto act, auto residual) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         constexpr bool RESIDUAL = decltype(residual)::value;
-        // rows whose residual is in flight together: what registers allow
-        constexpr int FIT = (TB == 8 ? 2 : 4) * 2 / (int)sizeof(O);
-        constexpr int BATCH = RESIDUAL && ACT >= 0 ? (ACT == kActGelu && FIT > 1 ? FIT / 2 : FIT) : 1;
-        const int64_t first = row0 + ei;
+        int64_t at = first * a.ldy + c;
+        if constexpr (RESIDUAL && ACT >= 0 && !EARLY) request_first();
         // both halves of a row one after the other: whole 128-byte lines
 #pragma unroll
-        for (int i0 = 0; i0 < TB; i0 += BATCH) {
-            int64_t row = first + 16 * i0;
-            asm volatile("" : "+v"(row));  // no addresses of later rows are held
-            Residual8<O> r[BATCH][HW];
-            if constexpr (RESIDUAL && ACT >= 0) {
+        for (int i = 0; i < TB; ++i) {
+            asm volatile("" : "+v"(at));
+            if (ACT < 0 && first + 16 * i >= a.M) break;
+            float v[HW][8];
 #pragma unroll
-                for (int i = i0; i < i0 + BATCH && i < TB; ++i)
+            for (int hw = 0; hw < HW; ++hw) {
+                f32x4(&s)[2] = z[i >> 2][hw][i & 3];
+                if (ACT >= 0) asm volatile("" : "+v"(s[0]), "+v"(s[1]));  // nothing of it is made ahead of the branches
 #pragma unroll
-                    for (int hw = 0; hw < HW; ++hw) r[i - i0][hw].request(a.R + (row + 16 * (i - i0)) * a.ldr + c + 32 * hw);
-            }
+                for (int q = 0; q < 8; ++q) v[hw][q] = s[q >> 2][q & 3];
+                const int kind = ACT >= 0 ? ACT : a.act;
+                if (sizeof(O) == 2 && kind == kActGelu) gelu_from<ACT >= 0 ? 8 : 1>(table, v[hw]);
+                else activate<sizeof(O) == 4>(v[hw], kind);
+                if constexpr (GATED) {
 #pragma unroll
-            for (int i = i0; i < i0 + BATCH && i < TB; ++i) {
-                const int64_t t = row + 16 * (i - i0);
-                if (ACT < 0 && t >= a.M) continue;
-#pragma unroll
-                for (int hw = 0; hw < HW; ++hw) {
-                    const int have = ACT >= 0 ? 8 : (int)max((int64_t)0, min((int64_t)8, a.N - c - 32 * hw));
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = z[i >> 2][hw][i & 3][q >> 2][q & 3];
-                    activate<sizeof(O) == 4>(v, ACT >= 0 ? ACT : a.act);
-                    if constexpr (GATED) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] *= z[i >> 2][1][i & 3][q >> 2][q & 3];
-                    }
-                    if constexpr (RESIDUAL && ACT >= 0) r[i - i0][hw].add_to(v);
-                    else if constexpr (RESIDUAL) add_row(v, a.R + t * a.ldr + c + 32 * hw, have);
-                    // Past the L2 where the residual's rows go through it too: 25728 x 1024 ->
-                    // 4096 194 us without, 177 with, 25728 x 4096 -> 1024 115 and 110.  Without a
-                    // residual it is 1 to 3 % either way: a tile waits longer for its stores.
-                    store_row<RESIDUAL && ACT >= 0>(a.Y + t * a.ldy + c + 32 * hw, v, have);
+                    for (int q = 0; q < 8; ++q) v[hw][q] *= z[i >> 2][1][i & 3][q >> 2][q & 3];
                 }
+                if constexpr (RESIDUAL && ACT >= 0) res[i % FIT][hw].add_to(v[hw]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (RESIDUAL && ACT >= 0) {
+                if (i + FIT < TB) request(i + FIT);
+            }
+#pragma unroll
+            for (int hw = 0; hw < HW; ++hw) {
+                const int have = ACT >= 0 ? 8 : (int)max((int64_t)0, min((int64_t)8, a.N - c - 32 * hw));
+                if constexpr (RESIDUAL && ACT < 0) add_row(v[hw], a.R + (first + 16 * i) * a.ldr + c + 32 * hw, have);
+                // Past the L2 where the residual's rows go through it too: 16384 x 14336 -> 4096
+                // 711 us without, 698 with, others 0 to 1 %.  Without a residual a tile waits
+                // longer for its stores: 16384 x 2048 -> 8192 259 us without, 301 with.
+                store_row<RESIDUAL && ACT >= 0>(a.Y + at + 32 * hw, v[hw], have);
+            }
+            at += step;
+            if (RESIDUAL || i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // every row: 1 to 2 % without a residual
         }
     };
     auto finish_act = [&](auto act) __attribute__((always_inline)) {

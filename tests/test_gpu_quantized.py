@@ -341,6 +341,32 @@ def test_gated(N, c1, c2, out):
         close(h, *gated_ref(x, sx, g, sg, u, su, *b, act, o), f"{act} {bias}")
 
 
+@pytest.mark.parametrize("c2", [2304, 4096])
+def test_gelu_of_large_tiles(c2):
+    """bf16 results of large tiles take Phi from lines of 1 / 256: off by h^2 t^2 / 16 of themselves at most (1.6e-4 at
+    12.9) and a rounding of each line's two coefficients (t^2 u each), from an argument off by 2 u (t^2 2 u)."""
+    import torch
+    N, c1 = 4096, 16
+    x, w = torch.zeros(N, c1, dtype=torch.int8), torch.zeros(c2, c1, dtype=torch.int8)
+    x[:, 3], w[:, 3] = 1, 1
+    sx, sw = torch.linspace(-13.0, 13.0, N), 1.0 - torch.arange(c2) * 2.0 ** -17
+    sx[:6] = torch.tensor([float("nan"), float("inf"), float("-inf"), -1e30, -13.3, 1e30])
+    d = [v.cuda() for v in (x, sx, w, sw)]
+    z = sx.double()[:, None] * sw.double()
+    t2 = z[6:] * z[6:]
+    ref = 0.5 * z[6:] * torch.special.erfc(-z[6:] * 0.5 ** 0.5)
+    bound = (half(torch.bfloat16) + 1.002 * (t2 + 1) / 16 / 65536 + 4 * U * (t2 + 2)) * ref.abs() + 1e-36
+    one = torch.ones(c2, dtype=torch.bfloat16, device="cuda")
+    linear = dyra.dyra_linear_quantized(*d, act="gelu").double().cpu()
+    gated = dyra.dyra_gated_quantized(*d, torch.zeros_like(d[2]), d[3], bias_u=one, act="gelu").double().cpu()
+    assert (linear[1] == float("inf")).all() and (linear[2] == 0).all()
+    assert gated[1:3].isnan().all()   # the up sums of 0 times an infinite scale
+    for y in (linear, gated):
+        assert y[0].isnan().all() and (y[3:5].abs() <= 1e-36).all()
+        assert ((y[5] / z[5] - 1).abs() <= half(torch.bfloat16)).all()
+        close(y[6:], ref, bound)
+
+
 # enough large tiles to fill the chip; one slab of K to several, whole and partial; rows and features past the last tile
 @pytest.mark.parametrize("N,c1,c2", [(4000, 16, 2050), (3841, 128, 2304), (4096, 144, 2048), (4100, 256, 2001), (3900, 384, 2100),
                                      (2100, 528, 4000), (4097, 640, 1930), (33000, 80, 100)])

@@ -389,7 +389,7 @@ template <typename E, typename O, bool GATED> hipError_t launch_linear(const Lin
     }
 }
 
-// K in parts.  us without | with (the tiles of ffn_choice.h, join included): see there.
+// K in parts, and their join (what it is worth: pick_split).
 template <typename O, bool GATED>
 hipError_t launch_split(const LinearArgs<i8, O> &a, const Split &s, int32_t *work, hipStream_t st) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;

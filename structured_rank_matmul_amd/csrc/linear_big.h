@@ -1,6 +1,6 @@
 // 256 x 256 tiles (224 and 192 x 256 too) of the linear layer and the gated pair, bf16 and 8-bit
-// integers (128 a slab row, epilogue in linear_scaled.h), for products that fill the chip: eight wavefronts in two groups of four that take turns on
-// the matrix cores.
+// integers (128 a slab row, epilogue in linear_scaled.h), for products that fill the chip:
+// eight wavefronts in two groups of four that take turns on the matrix cores.
 //
 // A workgroup owns 32 TB tokens and 256 weight rows (256 output features, or 128
 // gate and the same 128 up rows).  Wavefront (wm, wn) owns TB blocks of 16 tokens

@@ -5,9 +5,9 @@
 //     a = max |y| = rho max |z w|,  s = max(a, 127 2^-126) / 127,  q = nearest(y / s)
 //
 // The sum of squares and max |z w| do not wait for one another, so a row needs one
-// reduction.  s is taken from a normal float32 at least (2^-126 for a row of zeros): y / s
-// is y (127 / a), and neither factor leaves float32's range.  A row whose a is not finite
-// has s = NaN and q = 0: what is made of it is NaN.
+// reduction.  s is taken from a normal float32 at least (2^-126 for a row of zeros).  q is
+// 127 y / a (Steps), of which rho is no part: z w is measured by its own largest.  A row
+// whose a is not finite has s = NaN and q = 0: what is made of it is NaN.
 //
 // Squares past float32's range (|z| > 1.8e19) are summed again with z 2^-96, whose norm is
 // the same up to eps 2^-192, which is nothing beside them.
@@ -74,23 +74,38 @@ template <typename E> struct Chunk {
     __device__ __forceinline__ void store(E *p) const { __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(p)); }
 };
 
-// The whole number nearest to y * steps (|y * steps| < 2^21) in the low bits: added to
-// 1.5 2^23, a float32 whose last place is 1.
-__device__ __forceinline__ unsigned nearest(float y, float steps) {
-    return __float_as_uint(__builtin_fmaf(y, steps, 12582912.f));
-}
+// 127 y / top to the nearest whole number, halves to the even one, in a float32's low bits.
+// In bf16 rows every value of half the largest is such a half, so the ratio has to be right to
+// better than a float32 rounding: y steps alone is off by up to 2^-24 of itself, and those
+// values went to 63 or 64 as 127 / top happened to be rounded.  `rest`, what that rounding
+// left out, puts the ratio right to 2^-46 before its one rounding.  Two operations more a
+// value, under the loads: us without | with, bf16: 16384 x 14336 124.3 | 124.4, 25728 x 1024
+// 13.6 | 13.7, 16 x 14336 3.4 | 3.5, 2048 x 65536 (a row a CU) 74.9 | 76.1.
+struct Steps {
+    float steps, rest;
+    // top: 127 2^-126 .. 2^128, so that 127 / top is a normal float32 too
+    __device__ __forceinline__ explicit Steps(float top) : steps(127.f / top) {
+        rest = __builtin_fmaf(-steps, top, 127.f) * (1.f / 127.f);
+    }
+    __device__ __forceinline__ unsigned of(float y) const {
+        const float about = y * steps;
+        const float ratio = __builtin_fmaf(y, steps, about * rest);
+        return __float_as_uint(ratio + 12582912.f);  // 1.5 2^23: its last place is 1
+    }
+};
 // The low bytes of four.
 __device__ __forceinline__ unsigned bytes4(unsigned a, unsigned b, unsigned c, unsigned d) {
     const unsigned lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
     return lo | hi << 16;
 }
-template <int V> __device__ __forceinline__ void store_bytes(i8 *p, const unsigned (&q)[V]) {
+// Of V values, with `keep` 0 as zeros.
+template <int V> __device__ __forceinline__ void store_bytes(i8 *p, const unsigned (&q)[V], unsigned keep) {
     typedef unsigned u32_any __attribute__((aligned(1)));
     typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
     typedef u32x2 u32x2_any __attribute__((aligned(1)));
-    const unsigned lo = bytes4(q[0], q[1], q[2], q[3]);
+    const unsigned lo = bytes4(q[0], q[1], q[2], q[3]) & keep;
     if constexpr (V == 4) __builtin_nontemporal_store(lo, reinterpret_cast<u32_any *>(p));
-    else __builtin_nontemporal_store(u32x2{lo, bytes4(q[4], q[5], q[6], q[7])}, reinterpret_cast<u32x2_any *>(p));
+    else __builtin_nontemporal_store(u32x2{lo, bytes4(q[4], q[5], q[6], q[7]) & keep}, reinterpret_cast<u32x2_any *>(p));
 }
 
 // Threads of a workgroup: rows within a wavefront share one, longer rows have their own.
@@ -196,10 +211,14 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         rho = 1.f / sqrtf(v.sum / (float)c + a.eps * (by * by));
     }
     if constexpr (EIGHT) {
-        const float top = fmaxf(__uint_as_float(v.top) * rho, kLeastTop);
-        const bool finite = v.top < 0x7f800000u && top < INFINITY;
-        if (t == 0) a.scales[row] = finite ? top / 127.f : NAN;
-        const float steps = 127.f / top;
+        const float most = __uint_as_float(v.top), largest = most * rho;
+        const bool finite = v.top < 0x7f800000u && largest < INFINITY;
+        if (t == 0) a.scales[row] = finite ? fmaxf(largest, kLeastTop) / 127.f : NAN;
+        // Where scales begin, and where 127 / max |z w| could leave float32's range, y itself is measured.
+        const bool as_y = !(largest >= kLeastTop && most >= 0x1p-100f);
+        const float by_w = as_y ? rho : 1.f;
+        const Steps to(as_y ? fmaxf(largest, kLeastTop) : most);
+        const unsigned keep = finite ? 0xffffffffu : 0u;
         i8 *const y = (i8 *)a.Y + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
@@ -208,11 +227,14 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
             if (k < chunks) {
                 unsigned b[V];
 #pragma unroll
-                for (int q = 0; q < V; ++q) b[q] = finite ? nearest(z[i][q] * by * weight(i, q) * rho, steps) : 0u;
-                store_bytes<V>(y + k * V, b);
+                for (int q = 0; q < V; ++q) {
+                    const float value = z[i][q] * by * weight(i, q);
+                    b[q] = to.of(NORM ? value * by_w : value);
+                }
+                store_bytes<V>(y + k * V, b, keep);
             }
         }
-        if (last) y[rest] = (i8)(finite ? nearest(z1 * by * w1 * rho, steps) : 0u);
+        if (last) y[rest] = (i8)(to.of(z1 * by * w1 * by_w) & keep);
     } else {
         E *const y = (E *)a.Y + row * a.ldy;
 #pragma unroll

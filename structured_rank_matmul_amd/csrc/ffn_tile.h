@@ -165,12 +165,26 @@ template <typename T> struct Residual8 {
 #pragma unroll
         for (int q = 0; q < 8 * (int)sizeof(T) / 16; ++q) c[q] = *reinterpret_cast<const u32x4_any *>((const char *)p + 16 * q);
     }
-    __device__ __forceinline__ void add_to(float (&v)[8]) const {
+    __device__ __forceinline__ void values(float (&r)[8]) const {
         union { u32x4 u[8 * sizeof(T) / 16]; T e[8]; } w;
 #pragma unroll
         for (int q = 0; q < 8 * (int)sizeof(T) / 16; ++q) w.u[q] = c[q];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += to_f32(w.e[q]);
+        for (int q = 0; q < 8; ++q) r[q] = to_f32(w.e[q]);
+    }
+    __device__ __forceinline__ void add_to(float (&v)[8]) const {
+        float r[8];
+        values(r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += r[q];
+    }
+    // The same as an addition of its own: a product that v was made by just before is rounded first.
+    __device__ __forceinline__ void add_rounded(float (&v)[8]) const {
+#pragma clang fp contract(off)
+        float r[8];
+        values(r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += r[q];
     }
 };
 // The same of a row of which the first `have` (0 .. 8) exist; columns past them

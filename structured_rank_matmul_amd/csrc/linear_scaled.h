@@ -119,7 +119,9 @@ __device__ __forceinline__ void scaled_epilogue(const LinearArgs<i8, O> &a, cons
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[hw][q] *= z[i >> 2][1][i & 3][q >> 2][q & 3];
                 }
-                if constexpr (RESIDUAL && ACT >= 0) res[i % FIT][hw].add_to(v[hw]);
+                // The activation's last product and this addition would make one FMA here, where ACT is
+                // known, and in no kernel that asks for it at run time: other bits.
+                if constexpr (RESIDUAL && ACT >= 0) res[i % FIT][hw].add_rounded(v[hw]);
             }
             if constexpr (RESIDUAL && ACT >= 0) {
                 if (i + FIT < TB) request(i + FIT);

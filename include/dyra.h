@@ -400,7 +400,9 @@ dyra_status dyra_dequantize(const int8_t *Q, int64_t ldq, const float *scales, i
  * bias[j]) + residual.  X device int8 [N][c1], Wt device int8 [c2][c1], any values -128 ..
  * 127; x_scales device float32 [N], w_scales device float32 [c2]; bias device, out_dtype,
  * [c2], or NULL; residual and Y device, out_dtype, [N][c2].  The sums are exact, in 32-bit
- * integers.  c1, ldx and ldw are multiples of 16 (DYRA_ERR_SHAPE, DYRA_ERR_ALIGN), ldx, ldw
+ * integers.  Scales of 2^-126 to 2^97 in magnitude, zeros too, keep the products accurate wherever
+ * float32 holds them; a weight's scale above 2^97 may take one past its range that a small
+ * scale of the token would bring back.  c1, ldx and ldw are multiples of 16 (DYRA_ERR_SHAPE, DYRA_ERR_ALIGN), ldx, ldw
  * <= 2^20; everything else as for dyra_linear.
  *
  * workspace device, 16-byte aligned, or NULL.  With dyra_quantized_workspace_bytes() bytes a

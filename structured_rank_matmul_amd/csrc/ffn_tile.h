@@ -40,11 +40,13 @@ template <> struct Sums<i8> { typedef i32x4 type; };
 template <typename E> constexpr int slab_steps() { return sizeof(E) == 4 ? 1 : 2; }
 
 // A result before its activation: a sum with its bias, or of 8-bit operands with its
-// scales.  The scales' product is taken first: it leaves float32's range only with the
-// result.
+// scales.  The sum, a whole number up to 2^30, meets the weight's scale first: that is
+// neither subnormal nor past float32's range for scales of 2^-126 (the least that a
+// quantised row has) to 2^97, where the product of two scales may be either while the
+// result is not, and a sum of 0 stays 0 (0 times a product past the range is NaN).
 __device__ __forceinline__ float biased(float sum, float, float, float b) { return sum + b; }
 __device__ __forceinline__ float biased(int sum, float sx, float sw, float b) {
-    return __builtin_fmaf((float)sum, sx * sw, b);
+    return __builtin_fmaf((float)sum * sw, sx, b);
 }
 
 // A buffer resource over `bytes` (at most 2 GiB) from `p` on; loads past them, at

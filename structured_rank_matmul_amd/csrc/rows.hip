@@ -10,7 +10,8 @@
 // whose a is not finite has s = NaN and q = 0: what is made of it is NaN.
 //
 // Squares past float32's range (|z| > 1.8e19) are summed again with z 2^-96, whose norm is
-// the same up to eps 2^-192, which is nothing beside them.
+// the same up to eps 2^-192, which is nothing beside them.  Results are made of z 2^-48, so
+// that small values of such a row keep their bits.
 #include "ffn_tile.h"
 
 #include <algorithm>
@@ -236,6 +237,10 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         }
         if (last) y[rest] = (i8)(to.of(z1 * by * w1 * by_w) & keep);
     } else {
+        if (by < 1.f) {  // the other half of 2^-96 goes into rho: z by is subnormal only where z rho is
+            by = 0x1p-48f;
+            rho *= by;
+        }
         E *const y = (E *)a.Y + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {

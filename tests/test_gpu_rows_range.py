@@ -1,0 +1,29 @@
+"""Norms of rows whose values span much of float32's range: what is made on the way (z 2^-96 of rows whose squares leave
+the range) must not fall below it where the result does not."""
+import pytest
+
+from structured_rank_matmul_amd import dyra
+from test_gpu_ffn import half, rand, types
+from test_gpu_quantized import check_rows, norm_ref, relative
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [64, 1000, 4100, 40000])
+def test_small_values_beside_one_whose_square_is_past_the_range(c, dtype):
+    """One value of 2^70, others from 2^-48 on: results from 2^-118 on are normal numbers, right to the bound of any other."""
+    import torch
+    t = types()[dtype]
+    g = torch.Generator().manual_seed(c)
+    x = torch.ldexp(rand((12, c), 1, torch.float32).abs() + 1, torch.randint(-48, 30, (12, c), generator=g)).to(t)
+    x[:, c // 3] = 2.0 ** 70
+    w = (rand((c,), 2, torch.float32).abs() + 1).to(t)
+    for weight in (None, w):
+        y = dyra.dyra_norm(x.cuda(), None if weight is None else weight.cuda(), 1e-5)
+        ref = norm_ref(x, weight, 1e-5, None)[1].abs()   # (check_norm allows 1e-30)
+        assert ref[ref > 0].min() > 2.0 ** -126
+        off = (y.cpu().double().abs() - ref).abs()
+        assert (off <= (relative(c) + half(t) * (1 + relative(c))) * ref).all(), float((off / ref).max())
+    q, scales = dyra.dyra_norm_quantize(x.cuda(), w.cuda(), 1e-5)
+    check_rows(q, scales, norm_ref(x, w, 1e-5, None)[1], True)

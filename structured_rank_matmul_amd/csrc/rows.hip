@@ -212,13 +212,17 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         rho = 1.f / sqrtf(v.sum / (float)c + a.eps * (by * by));
     }
     if constexpr (EIGHT) {
+        // Where z w nears the end of float32's range, or the scale its least value, y is measured itself,
+        // (z rho) w: rows of zeros too.
+        if (NORM && !(__uint_as_float(v.top) * rho >= kLeastTop && __uint_as_float(v.top) >= 0x1p-100f)) {
+            by *= rho;
+            rho = 1.f;
+            v = stats(by);
+        }
         const float most = __uint_as_float(v.top), largest = most * rho;
         const bool finite = v.top < 0x7f800000u && largest < INFINITY;
         if (t == 0) a.scales[row] = finite ? fmaxf(largest, kLeastTop) / 127.f : NAN;
-        // Where scales begin, and where 127 / max |z w| could leave float32's range, y itself is measured.
-        const bool as_y = !(largest >= kLeastTop && most >= 0x1p-100f);
-        const float by_w = as_y ? rho : 1.f;
-        const Steps to(as_y ? fmaxf(largest, kLeastTop) : most);
+        const Steps to(fmaxf(most, kLeastTop));
         const unsigned keep = finite ? 0xffffffffu : 0u;
         i8 *const y = (i8 *)a.Y + row * a.ldy;
 #pragma unroll
@@ -228,14 +232,11 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
             if (k < chunks) {
                 unsigned b[V];
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    const float value = z[i][q] * by * weight(i, q);
-                    b[q] = to.of(NORM ? value * by_w : value);
-                }
+                for (int q = 0; q < V; ++q) b[q] = to.of(z[i][q] * by * weight(i, q));
                 store_bytes<V>(y + k * V, b, keep);
             }
         }
-        if (last) y[rest] = (i8)(to.of(z1 * by * w1 * by_w) & keep);
+        if (last) y[rest] = (i8)(to.of(z1 * by * w1) & keep);
     } else {
         if (by < 1.f) {  // the other half of 2^-96 goes into rho: z by is subnormal only where z rho is
             by = 0x1p-48f;

@@ -1,10 +1,10 @@
-"""Norms of rows whose values span much of float32's range: what is made on the way (z 2^-96 of rows whose squares leave
-the range) must not fall below it where the result does not."""
+"""Norms of rows whose values or weights span much of float32's range: what is made on the way (z 2^-96 of rows whose
+squares leave the range, z w) must not fall below it where the result does not."""
 import pytest
 
 from structured_rank_matmul_amd import dyra
 from test_gpu_ffn import half, rand, types
-from test_gpu_quantized import check_rows, norm_ref, relative
+from test_gpu_quantized import check_rows, check_sum, norm_ref, relative
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,25 @@ def test_small_values_beside_one_whose_square_is_past_the_range(c, dtype):
         assert (off <= (relative(c) + half(t) * (1 + relative(c))) * ref).all(), float((off / ref).max())
     q, scales = dyra.dyra_norm_quantize(x.cuda(), w.cuda(), 1e-5)
     check_rows(q, scales, norm_ref(x, w, 1e-5, None)[1], True)
+
+
+# exponents of the values, of the weights and of eps: z w is below 2^-126 where z w / sqrt(mean z^2 + eps) is above it
+SMALL = [(-84, -84, -126), (-20, -117, -40), (-63, -60, -126), (-126, -20, -126), (100, -149, -20), (-20, -125, -126)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [3, 64, 1000, 4100, 40000])
+@pytest.mark.parametrize("ez,ew,ee", SMALL)
+def test_small_products_of_values_and_weights(c, dtype, ez, ew, ee):
+    import torch
+    t = types()[dtype]
+    x = torch.ldexp(rand((9, c), 3, torch.float32), torch.tensor(ez)).to(t)
+    r = torch.ldexp(rand((9, c), 4, torch.float32), torch.tensor(ez)).to(t)
+    w = torch.ldexp(rand((c,), 5, torch.float32), torch.tensor(ew)).to(t)
+    x[4], r[4] = 0.0, 0.0
+    z, y = norm_ref(x, w, 2.0 ** ee, r)
+    q, scales, s = dyra.dyra_norm_quantize(x.cuda(), w.cuda(), 2.0 ** ee, residual=r.cuda())
+    check_rows(q, scales, y, True)
+    assert (q[4] == 0).all() and scales[4] == 2.0 ** -126
+    if ez > -100:
+        check_sum(s, z)

@@ -120,30 +120,48 @@ constexpr int rows_threads(int row) { return row <= 64 ? 256 : row; }
 template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
 __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> a) {
     constexpr int V = Chunk<E>::V, ROWS = rows_threads(THREADS) / THREADS;
-    const int t = threadIdx.x % THREADS;
+    int t = threadIdx.x % THREADS;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
     if (ROWS > 1 && row >= a.N) return;  // all threads of a row, which wait for no others
     const int c = (int)a.c, chunks = c / V, rest = chunks * V + t;
     const bool last = rest < c;
     const E *const x = a.X + row * a.ldx, *const r = NORM && a.R ? a.R + row * a.ldr : nullptr;
 
+    // In the longest float32 rows z alone is 64 of a thread's 128 registers.  X and the residual are
+    // loaded half of the chunks at a time, weights four chunks at a time, and a chunk's place is
+    // computed anew for each use: without that 32 to 47 registers went to scratch.  us without |
+    // with, 2048 x 65536: norm 300 | 209, with residual 484 | 404 (5.3 TB/s), to 8 bits 320 | 183,
+    // with residual 485 | 363 (4.8 TB/s).
+    constexpr bool TIGHT = NORM && CHUNKS > 8;
+    constexpr int AT_ONCE = TIGHT ? CHUNKS / 2 : CHUNKS;
+    auto fresh = [&]() __attribute__((always_inline)) {
+        if (TIGHT) {
+            asm volatile("" : "+v"(t));
+            t &= THREADS - 1;
+        }
+    };
     float z[CHUNKS][V], z1 = 0.f;
-    {
-        Chunk<E> xs[CHUNKS], rs[CHUNKS];
+    if (last) z1 = to_f32(x[rest]) + (r ? to_f32(r[rest]) : 0.f);
 #pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
+    for (int from = 0; from < CHUNKS; from += AT_ONCE) {
+        Chunk<E> xs[AT_ONCE], rs[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
             xs[i].u = rs[i].u = u32x4{};
-            const int k = t + i * THREADS;
+            const int k = t + (from + i) * THREADS;
             if (k < chunks) {
                 xs[i].load(x + k * V);
                 if (r) rs[i].load(r + k * V);
             }
         }
-        if (last) z1 = to_f32(x[rest]) + (r ? to_f32(r[rest]) : 0.f);
 #pragma unroll
-        for (int i = 0; i < CHUNKS; ++i)
+        for (int i = 0; i < AT_ONCE; ++i)
 #pragma unroll
-            for (int q = 0; q < V; ++q) z[i][q] = to_f32(xs[i].e[q]) + (r ? to_f32(rs[i].e[q]) : 0.f);
+            for (int q = 0; q < V; ++q) {
+                z[from + i][q] = to_f32(xs[i].e[q]) + (r ? to_f32(rs[i].e[q]) : 0.f);
+                if (TIGHT) asm volatile("" : "+v"(z[from + i][q]));  // made here, before the other half is asked for
+            }
+        fresh();
     }
     if (NORM && a.S) {
         E *const s = a.S + row * a.lds;
@@ -188,6 +206,7 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
     auto weight = [&](int i, int q) { return weighted ? to_f32(ws[HELD ? i : 0].e[q]) : 1.f; };
     auto stats = [&](float by) {
         RowStats v = {0.f, 0u};
+        fresh();
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             if (EIGHT) weights(i);
@@ -197,6 +216,7 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
                 if (NORM) v.sum = __builtin_fmaf(y, y, v.sum);
                 if (EIGHT) v.top = max(v.top, __float_as_uint(y * weight(i, q)) & 0x7fffffffu);
             }
+            if (TIGHT && i % 4 == 3) asm volatile("" : "+v"(v.top));  // four chunks of weights at a time
         }
         if (NORM) v.sum = __builtin_fmaf(z1 * by, z1 * by, v.sum);
         if (EIGHT) v.top = max(v.top, __float_as_uint(z1 * by * w1) & 0x7fffffffu);
@@ -223,6 +243,7 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         const bool finite = v.top < 0x7f800000u && largest < INFINITY;
         if (t == 0) a.scales[row] = finite ? fmaxf(largest, kLeastTop) / 127.f : NAN;
         const Steps to(fmaxf(most, kLeastTop));
+        fresh();
         const unsigned keep = finite ? 0xffffffffu : 0u;
         i8 *const y = (i8 *)a.Y + row * a.ldy;
 #pragma unroll
@@ -242,6 +263,7 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
             by = 0x1p-48f;
             rho *= by;
         }
+        fresh();
         E *const y = (E *)a.Y + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {

@@ -79,18 +79,18 @@ template <typename E> struct Chunk {
 // In bf16 rows every value of half the largest is such a half, so the ratio has to be right to
 // better than a float32 rounding: y steps alone is off by up to 2^-24 of itself, and those
 // values went to 63 or 64 as 127 / top happened to be rounded.  `rest`, what that rounding
-// left out, puts the ratio right to 2^-46 before its one rounding.  Two operations more a
-// value, under the loads: us without | with, bf16: 16384 x 14336 124.3 | 124.4, 25728 x 1024
-// 13.6 | 13.7, 16 x 14336 3.4 | 3.5, 2048 x 65536 (a row a CU) 74.9 | 76.1.
+// left out, puts the ratio right to 2^-46 before its one rounding, and still to 2^-28 where
+// rest is subnormal (top above 2^102).  Two operations more a value, under the loads of long
+// rows: us without | with, bf16: 16384 x 14336 123.5 | 123.5, 2048 x 65536 (a row a CU) 75.2 |
+// 76.1, 16 x 14336 3.4 | 3.5, norms of 32768 x 200 7.4 | 7.8.
 struct Steps {
     float steps, rest;
     // top: 127 2^-126 .. 2^128, so that 127 / top is a normal float32 too
     __device__ __forceinline__ explicit Steps(float top) : steps(127.f / top) {
-        rest = __builtin_fmaf(-steps, top, 127.f) * (1.f / 127.f);
+        rest = __builtin_fmaf(-steps, top, 127.f) * (1.f / 127.f) * steps;
     }
     __device__ __forceinline__ unsigned of(float y) const {
-        const float about = y * steps;
-        const float ratio = __builtin_fmaf(y, steps, about * rest);
+        const float ratio = __builtin_fmaf(y, steps, y * rest);
         return __float_as_uint(ratio + 12582912.f);  // 1.5 2^23: its last place is 1
     }
 };

@@ -95,11 +95,14 @@ inline Tile pick_tile(int elem, bool gated, int64_t M, int64_t N, int64_t row_by
 // as many workgroups each, joined by a second kernel.  It pays for long rows and few tiles;
 // the second kernel and the workspace cost 6 us.  The times of the tiles above are
 // those of short rows: over long ones the smaller tiles took up to 1.5 times as long, parts of
-// them 1.2 times (fitted to 90 products of 33 to 8000 tokens: the choice is 0.7 % behind
-// the best of all on average, never to split 7 %).  us, whole | split: 186 x 12416 -> 188
-// 19.2 | 10.3, 64 x 14336 -> 4096 28.7 | 19.2, 185 x 11072 -> 1600 19.2 | 14.4, gated 1102 x
-// 10288 -> 456 38.9 | 28.0, 166 x 10320 -> 3968 54.9 | 43.9; left whole: 64 x 4096 -> 4096 8.9
-// | 10.8, 512 x 4096 -> 4096 14.9 | 22.8, 583 x 5808 -> 3957 31.7 | 32.2.
+// them 1.2 times (a fit to 90 products of 33 to 8000 tokens).  67 products that this splits took
+// 0.62 of the whole's time on average, 0.98 at worst.  us, inputs past the caches, whole | split:
+// 186 x 12416 -> 188 22.6 | 11.3, 64 x 14336 -> 4096 29.1 | 20.6, 185 x 11072 -> 1600 25.7 | 20.6,
+// gated 1102 x 10288 -> 456 48.3 | 33.7, 166 x 10320 -> 3968 40.3 | 37.1, 583 x 5808 -> 3957 43.8 |
+// 39.1; left whole: 64 x 4096 -> 4096 11.0 | 11.7, 256 x 4096 -> 4096 13.1 | 18.6, 512 x 4096 ->
+// 4096 19.2 | 26.9, and, which it should split, gated 51 x 5584 -> 854 20.2 | 14.1.  The whole is
+// priced with `once`, as in the fit: with tile_once() 14 products of rows of 37000 to 46000, which
+// take 0.79 of the time split (gated 1597 x 40400 -> 1290 366 | 280), would be left whole.
 struct Split {
     Tile tile;
     int parts;   // 1: no split

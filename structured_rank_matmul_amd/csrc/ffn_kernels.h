@@ -90,7 +90,7 @@ template <typename E> hipError_t launch_moe(const MoeArgs<E> &a, hipStream_t st)
 // Root-mean-square norm of rows (W null: ones), E rows; Y of E or, in 8 bits with a
 // scale for each row, of i8:
 //   z = X + R,  S = z,  Y = z / sqrt(mean z^2 + eps) * W
-// and, with `norm` false, quantisation of X.
+// launch_quantize makes 8-bit rows of X alone: y = X.
 template <typename E> struct RowArgs {
     const E *X;
     int64_t ldx;

@@ -6,7 +6,8 @@
 // a bf16 rounding: 3.9e-3).  Below it ends in 0.
 //
 // Six vector instructions and a read of 8 bytes a value, which runs beside them, for 13 and an
-// exponential.  25728 x 1024 -> 4096: 144 us, with gelu_erf 170, without an activation 130.
+// exponential.  25728 x 1024 -> 4096 with bias: 145 us, with gelu_erf 168, without an activation 132;
+// gated 16384 x 4096 -> 14336 1406 and 1448.
 #pragma once
 
 #include "ffn_tile.h"

@@ -114,9 +114,9 @@ constexpr int rows_threads(int row) { return row <= 64 ? 256 : row; }
 
 // THREADS threads hold a row of up to THREADS * CHUNKS whole 16-byte chunks, and one
 // more element each of the rest: it is read once, all its loads in flight together.  Bound
-// by memory: 16384 x 4096 bf16 with residual 76 us to 8 bits (6.2 TB/s of read and
-// written bytes) and 89 to bf16 (6.0); quantisation 34 us (5.9), 16384 x 14336 121 (5.8).
-// One workgroup a row that was read twice, by elements: 255, 105 at 25728 x 1024 (37), 330.
+// by memory: 16384 x 4096 bf16 with residual 80 us to 8 bits (5.9 TB/s of read and
+// written bytes) and 93 to bf16 (5.8); quantisation 36 us (5.6), 16384 x 14336 124 (5.7).
+// One workgroup a row that was read twice, by elements: 255 to 8 bits, 330 the last.
 template <typename E, bool NORM, bool EIGHT, int THREADS, int CHUNKS>
 __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> a) {
     constexpr int V = Chunk<E>::V, ROWS = rows_threads(THREADS) / THREADS;

@@ -384,7 +384,7 @@ dyra_status dyra_norm_quantize(const void *X, int64_t ldx, int64_t N, int64_t c,
  * number nearest to X[i][j] / (that maximum / 127), -127 .. 127; a half goes to the even one (a
  * float32 value within 2^-23 of itself of a half, but not on it, may go to either).
  * A row of zeros has the scale 2^-126.  A row with an infinity or a NaN (for
- * dyra_norm_quantize also one whose results, or whose Z * weight, leave float32's range) has
+ * dyra_norm_quantize also one whose results leave float32's range) has
  * the scale NaN and the values 0, so that what is made of it is NaN.  X device, dtype, [N][c], aligned to
  * its elements; Q device int8 [N][c]; scales device float32 [N].
  */

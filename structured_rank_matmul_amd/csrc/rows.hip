@@ -232,9 +232,10 @@ __global__ __launch_bounds__(rows_threads(THREADS)) void rows_kernel(RowArgs<E> 
         rho = 1.f / sqrtf(v.sum / (float)c + a.eps * (by * by));
     }
     if constexpr (EIGHT) {
-        // Where z w nears the end of float32's range, or the scale its least value, y is measured itself,
-        // (z rho) w: rows of zeros too.
-        if (NORM && !(__uint_as_float(v.top) * rho >= kLeastTop && __uint_as_float(v.top) >= 0x1p-100f)) {
+        // Where z w leaves float32's range or nears its end, or the scale its least value, y is measured
+        // itself, (z rho) w: rows of zeros and of infinities too.
+        const float zw = __uint_as_float(v.top);
+        if (NORM && !(zw * rho >= kLeastTop && zw >= 0x1p-100f && zw < INFINITY)) {
             by *= rho;
             rho = 1.f;
             v = stats(by);

@@ -49,3 +49,20 @@ def test_small_products_of_values_and_weights(c, dtype, ez, ew, ee):
     assert (q[4] == 0).all() and scales[4] == 2.0 ** -126
     if ez > -100:
         check_sum(s, z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [3, 64, 1000, 4100, 40000])
+@pytest.mark.parametrize("ez,ew", [(60, 90), (100, 120), (40, 124)])
+def test_large_products_of_values_and_weights(c, dtype, ez, ew):
+    """z w is past float32's range, the results are not: the largest is below 2^(ew + 3) sqrt(c)."""
+    import torch
+    t = types()[dtype]
+    x = torch.ldexp(rand((9, c), 6, torch.float32), torch.tensor(ez)).to(t)
+    w = torch.ldexp(rand((c,), 7, torch.float32).clamp(-3, 3), torch.tensor(min(ew, 118))).to(t)
+    x[4] = 0.0
+    y = norm_ref(x, w, 1e-5, None)[1]
+    assert torch.finfo(torch.float32).max > y.abs().max() and (x.double() * w.double()).abs().max() > 2.0 ** 128
+    q, scales = dyra.dyra_norm_quantize(x.cuda(), w.cuda(), 1e-5)
+    check_rows(q, scales, y, True)
+    assert (q[4] == 0).all() and scales[4] == 2.0 ** -126
